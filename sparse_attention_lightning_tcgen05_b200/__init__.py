@@ -31,13 +31,17 @@ DSA_MASK_COMPRESSED = 2
 DSA_MASK_BOUND = float.fromhex("-0x1.FEp127")
 DSA_FLAG_SCORES_IN_WORKSPACE = 1
 DSA_FLAG_SELFTEST_STALL = 2
+DSA_ROPE_INTERLEAVED = 0
+DSA_ROPE_HALVES = 1
 
-# Every symbol include/dsa_indexer.h and include/dsa_sparse_mqa.h declare.
+# Every symbol the headers under include/ declare.
 EXPORTS = ("dsa_indexer_workspace_size", "dsa_indexer_score", "dsa_indexer_topk",
            "dsa_indexer_forward", "dsa_indexer_forward_noalloc",
            "dsa_indexer_get_error", "dsa_sparse_mqa_workspace_size",
            "dsa_sparse_mqa_forward", "dsa_indexer_prepare_workspace_size",
-           "dsa_indexer_prepare", "dsa_status_string")
+           "dsa_indexer_prepare", "dsa_cache_append", "dsa_block_pool",
+           "dsa_paged_attention_workspace_size", "dsa_paged_attention_forward",
+           "dsa_block_attention_forward", "dsa_status_string")
 
 
 class dsa_indexer_desc_t(ctypes.Structure):
@@ -65,6 +69,35 @@ class dsa_prepare_desc_t(ctypes.Structure):
                 ("rope_dim", ctypes.c_int32), ("k_norm_eps", ctypes.c_float),
                 ("w_scale", ctypes.c_float), ("S", ctypes.c_int64),
                 ("k_seq_stride", ctypes.c_int64), ("wait_limit_ns", ctypes.c_uint64)]
+
+
+class dsa_paged_cache_t(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p)]
+
+
+class dsa_append_desc_t(ctypes.Structure):
+    _fields_ = [("cache", dsa_paged_cache_t), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("rope", ctypes.c_int),
+                ("q_dtype", ctypes.c_int), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class dsa_block_pool_desc_t(ctypes.Structure):
+    _fields_ = [("cache", dsa_paged_cache_t), ("block_size", ctypes.c_int32),
+                ("S_pool", ctypes.c_int64), ("seq_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class dsa_paged_attention_desc_t(ctypes.Structure):
+    _fields_ = [("cache", dsa_paged_cache_t), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("block_heads", ctypes.c_int32), ("wait_limit_ns", ctypes.c_uint64)]
 
 
 class DsaError(RuntimeError):
@@ -95,6 +128,12 @@ _lib.dsa_sparse_mqa_forward.argtypes = [_M, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _
 _R = ctypes.POINTER(dsa_prepare_desc_t)
 _lib.dsa_indexer_prepare_workspace_size.argtypes = [_R, ctypes.POINTER(_sz)]
 _lib.dsa_indexer_prepare.argtypes = [_R] + [_vp] * 14 + [_sz, _vp]
+_lib.dsa_cache_append.argtypes = [ctypes.POINTER(dsa_append_desc_t)] + [_vp] * 13 + [_vp]
+_lib.dsa_block_pool.argtypes = [ctypes.POINTER(dsa_block_pool_desc_t)] + [_vp] * 7 + [_vp]
+_A = ctypes.POINTER(dsa_paged_attention_desc_t)
+_lib.dsa_paged_attention_workspace_size.argtypes = [_A, ctypes.POINTER(_sz)]
+_lib.dsa_paged_attention_forward.argtypes = [_A] + [_vp] * 11 + [_sz, _vp]
+_lib.dsa_block_attention_forward.argtypes = [_A] + [_vp] * 12 + [_sz, _vp]
 _lib.dsa_status_string.argtypes = [ctypes.c_int]
 _lib.dsa_status_string.restype = ctypes.c_char_p
 for _f in EXPORTS[:-1]:
@@ -244,3 +283,101 @@ def dsa_indexer_prepare(desc, x, qr, wq_b, wk, weights_proj, k_norm_weight, k_no
         _ptr(k_norm_weight), _ptr(k_norm_bias), _ptr(cos), _ptr(sin), _ptr(positions),
         _ptr(q_out), _ptr(w_out), _ptr(key_cache), _ptr(workspace), workspace_bytes,
         stream), "dsa_indexer_prepare")
+
+
+def _device_ptrs(where, *xs):
+    """Device pointers of tensors, ints or None. A tensor that is not on the
+    current CUDA device is refused: the library launches on that device."""
+    out, current = [], None
+    for x in xs:
+        if x is None or isinstance(x, int):
+            out.append(x)
+            continue
+        if current is None:
+            import torch
+            current = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        if x.get_device() != current or current < 0:
+            raise ValueError(f"{where}: a tensor on {x.device}, the current CUDA device is "
+                             f"{current if current >= 0 else 'none'}")
+        out.append(x.data_ptr())
+    return out
+
+
+def make_paged_cache(page_size, pages_per_seq, num_pages, block_table, *, num_seqs, H_kv=1,
+                     D=128, dtype=DSA_KV_BF16, page_stride=None, slot_stride=None,
+                     head_stride=None):
+    """A paged cache. The strides default to pools [num_pages, page_size,
+    H_kv, D]; block_table: int32 [num_seqs, pages_per_seq], kept alive by the
+    caller while descriptors made of this one are used."""
+    return dsa_paged_cache_t(num_seqs=num_seqs, H_kv=H_kv, D=D, page_size=page_size,
+                             pages_per_seq=pages_per_seq, num_pages=num_pages, dtype=dtype,
+                             page_stride=page_size * H_kv * D if page_stride is None else page_stride,
+                             slot_stride=H_kv * D if slot_stride is None else slot_stride,
+                             head_stride=D if head_stride is None else head_stride,
+                             block_table=_ptr(block_table))
+
+
+def make_append_desc(cache, T, H, rope_dim, *, rope_style=DSA_ROPE_INTERLEAVED,
+                     q_dtype=DSA_KV_BF16, q_stride=None, k_stride=None, v_stride=None):
+    """Strides: elements between consecutive tokens of q, k and v (default:
+    contiguous [T, heads, D])."""
+    kv = cache.H_kv * cache.D
+    return dsa_append_desc_t(cache=cache, T=T, H=H, rope_dim=rope_dim, rope=rope_style,
+                             q_dtype=q_dtype, q_stride=H * cache.D if q_stride is None else q_stride,
+                             k_stride=kv if k_stride is None else k_stride,
+                             v_stride=kv if v_stride is None else v_stride)
+
+
+def dsa_cache_append(desc, q, k, v, cos, sin, positions, seq_ids, q_out, q_scale, k_cache,
+                     k_scale, v_cache, v_scale, stream=None) -> int:
+    return _check(_lib.dsa_cache_append(
+        ctypes.byref(desc), *_device_ptrs("dsa_cache_append", q, k, v, cos, sin, positions, seq_ids,
+                                          q_out, q_scale, k_cache, k_scale, v_cache, v_scale),
+        stream), "dsa_cache_append")
+
+
+def make_block_pool_desc(cache, block_size, S_pool, *, seq_stride=None, head_stride=None):
+    """The strides default to pooled rows [num_seqs, H_kv, S_pool, D]."""
+    head = S_pool * cache.D if head_stride is None else head_stride
+    return dsa_block_pool_desc_t(cache=cache, block_size=block_size, S_pool=S_pool,
+                                 seq_stride=cache.H_kv * head if seq_stride is None else seq_stride,
+                                 head_stride=head)
+
+
+def dsa_block_pool(desc, k_cache, k_scale, start, positions, pooled, pooled_scale, last_block=None,
+                   stream=None) -> int:
+    return _check(_lib.dsa_block_pool(
+        ctypes.byref(desc), *_device_ptrs("dsa_block_pool", k_cache, k_scale, start, positions,
+                                          pooled, pooled_scale, last_block), stream),
+        "dsa_block_pool")
+
+
+def make_paged_attention_desc(cache, T, H, sm_scale, *, window=0, block_size=0, num_blocks=0,
+                              block_heads=1, wait_limit_ns=0):
+    """block_size and num_blocks: for dsa_block_attention_forward."""
+    return dsa_paged_attention_desc_t(cache=cache, T=T, H=H, sm_scale=sm_scale, window=window,
+                                      block_size=block_size, num_blocks=num_blocks,
+                                      block_heads=block_heads, wait_limit_ns=wait_limit_ns)
+
+
+def dsa_paged_attention_workspace_size(desc) -> int:
+    n = _sz(0)
+    _check(_lib.dsa_paged_attention_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "dsa_paged_attention_workspace_size")
+    return n.value
+
+
+def dsa_paged_attention_forward(desc, q, k, k_scale, v, v_scale, sinks, positions, seq_ids, out,
+                                lse, workspace, workspace_bytes, stream=None) -> int:
+    return _check(_lib.dsa_paged_attention_forward(
+        ctypes.byref(desc), *_device_ptrs("dsa_paged_attention_forward", q, k, k_scale, v, v_scale,
+                                          sinks, positions, seq_ids, out, lse, workspace),
+        workspace_bytes, stream), "dsa_paged_attention_forward")
+
+
+def dsa_block_attention_forward(desc, q, k, k_scale, v, v_scale, sinks, positions, seq_ids, blocks,
+                                out, lse, workspace, workspace_bytes, stream=None) -> int:
+    return _check(_lib.dsa_block_attention_forward(
+        ctypes.byref(desc), *_device_ptrs("dsa_block_attention_forward", q, k, k_scale, v, v_scale,
+                                          sinks, positions, seq_ids, blocks, out, lse, workspace),
+        workspace_bytes, stream), "dsa_block_attention_forward")
