@@ -74,7 +74,7 @@ typedef struct {
   int32_t num_pages;       /* pages of the pools, >= 1, with
                               num_pages * page_size < 2^31                      */
   dsa_kv_dtype_t dtype;    /* of the key and value pools                        */
-  int64_t page_stride;     /* elements, multiples of 128, >= 0: between pages,  */
+  int64_t page_stride;     /* elements, multiples of 128, > 0: between pages,   */
   int64_t slot_stride;     /* between the slots of a page                       */
   int64_t head_stride;     /* and between the heads of a slot                   */
   const int32_t *block_table; /* device [num_seqs, pages_per_seq]               */

@@ -236,8 +236,11 @@ def raw_status(fn_name: str, *args) -> int:
 
 
 def current_stream_handle():
-    """The cudaStream_t of torch's current CUDA stream."""
+    """The cudaStream_t of torch's current CUDA stream (of the current device)."""
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 0.3 us; the object below, 3 us
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -288,19 +291,20 @@ def dsa_indexer_prepare(desc, x, qr, wq_b, wk, weights_proj, k_norm_weight, k_no
 def _device_ptrs(where, *xs):
     """Device pointers of tensors, ints or None. A tensor that is not on the
     current CUDA device is refused: the library launches on that device."""
-    out, current = [], None
-    for x in xs:
-        if x is None or isinstance(x, int):
-            out.append(x)
-            continue
-        if current is None:
-            import torch
-            current = torch.cuda.current_device() if torch.cuda.is_available() else -1
-        if x.get_device() != current or current < 0:
-            raise ValueError(f"{where}: a tensor on {x.device}, the current CUDA device is "
-                             f"{current if current >= 0 else 'none'}")
-        out.append(x.data_ptr())
-    return out
+    import torch
+    try:
+        current = torch.cuda.current_device()
+    except (RuntimeError, AssertionError):        # no CUDA device, or no CUDA in torch
+        current = -2
+    # get_device() is -1 for host memory
+    return [x if x is None or isinstance(x, int) else
+            x.data_ptr() if x.get_device() == current else _other_device(where, x, current)
+            for x in xs]
+
+
+def _other_device(where, x, current):
+    raise ValueError(f"{where}: a tensor on {x.device}, the current CUDA device is "
+                     f"{current if current >= 0 else 'none'}")
 
 
 def make_paged_cache(page_size, pages_per_seq, num_pages, block_table, *, num_seqs, H_kv=1,

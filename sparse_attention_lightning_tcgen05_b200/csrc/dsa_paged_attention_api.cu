@@ -20,6 +20,8 @@ namespace {
 // workspace size depends on the descriptor alone.
 constexpr int kPaCtasPerSm = 2;
 constexpr int kPaGrid = 148 * kPaCtasPerSm;
+constexpr uint64_t kPaWaitLimitNs = 4000000000ull;
+constexpr uint64_t kPaDrainLimitNs = 4000000000ull;
 
 dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
   if (!d) return DSA_ERR_INVALID_ARG;
@@ -30,6 +32,9 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
     return DSA_ERR_INVALID_ARG;
   if (d->H / d->cache.H_kv > 128) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->T) * d->H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  // a tensor map's strides are below 2^40 bytes
+  for (const int64_t s : {d->cache.page_stride, d->cache.slot_stride, d->cache.head_stride})
+    if (s >= int64_t{1} << 39) return DSA_ERR_UNSUPPORTED;
   if (list) {
     if (d->block_size < 1 || d->block_size > 65536 || (d->block_size & (d->block_size - 1)) != 0)
       return DSA_ERR_INVALID_ARG;
@@ -49,18 +54,33 @@ size_t workspace_bytes_needed() {
 }
 
 template <bool kFp8, bool kList>
-dsa_status_t launch(const dsa::PagedAttnParams &p, int grid, DeviceInfo *dev, uint32_t bit,
-                    cudaStream_t s) {
+dsa_status_t launch(const dsa::PagedAttnParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                    const CUtensorMap &tv, int grid, DeviceInfo *dev, uint32_t bit, cudaStream_t s) {
   const int smem = dsa::PaSmem<kFp8>::kTotal;
   const dsa_status_t st = ensure_smem_attr(dev, bit, dsa::paged_attention_kernel<kFp8, kList>, smem);
   if (st != DSA_OK) return st;
   if (launch_pdl(dsa::paged_attention_kernel<kFp8, kList>, grid, dsa::kPaThreads,
-                 static_cast<size_t>(smem), s, 0, p) != cudaSuccess)
+                 static_cast<size_t>(smem), s, 0, tq, tk, tv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   if (launch_pdl(dsa::paged_attention_join_kernel, grid * (dsa::kPaRows / 2), dsa::kPaJoinThreads, 0,
-                 s, 0, p, grid) != cudaSuccess)
+                 s, 0, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   return DSA_OK;
+}
+
+// A pool [num_pages][H_kv][page_size] of rows of 128, boxes of `rows` slots and
+// 128 bytes.
+dsa_status_t pool_map(CUtensorMap *m, const dsa_paged_cache_t *c, const void *base, int rows) {
+  const bool fp8 = c->dtype != DSA_KV_BF16;
+  const cuuint64_t elt = fp8 ? 1 : 2;
+  const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->H_kv), static_cast<cuuint64_t>(c->num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->slot_stride) * elt,
+                                 static_cast<cuuint64_t>(c->head_stride) * elt,
+                                 static_cast<cuuint64_t>(c->page_stride) * elt};
+  const cuuint32_t box[4] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(rows), 1, 1};
+  return make_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base,
+                  dims, strides, box);
 }
 
 dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *q, const void *k,
@@ -91,23 +111,20 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   p.G = d->H / d->cache.H_kv;
   p.head_tiles = (p.G + dsa::kPaRows - 1) / dsa::kPaRows;
   p.window = d->window;
-  p.gran_shift = 4;
-  int64_t most_chunks = (p.g.capacity() + dsa::kPaChunk - 1) / dsa::kPaChunk;
+  p.gran_shift = std::min(5, p.g.page_shift);
+  int64_t most_steps = (p.g.capacity() + dsa::kPaStep - 1) / dsa::kPaStep;
   if (d->window > 0 || list)       // a window may begin inside a step
-    most_chunks = std::min<int64_t>(most_chunks, (static_cast<int64_t>(d->window) + 15) / 16 + 1);
+    most_steps = std::min<int64_t>(most_steps, d->window / dsa::kPaStep + 2);
   if (list) {
     p.block_shift = __builtin_ctz(static_cast<unsigned>(d->block_size));
     p.num_blocks = d->num_blocks;
     p.block_heads = d->block_heads;
-    p.gran_shift = std::min(4, p.block_shift);
-    p.list_chunks = static_cast<int>(
-        (static_cast<int64_t>(d->num_blocks) * d->block_size + dsa::kPaChunk - 1) / dsa::kPaChunk);
-    most_chunks += p.list_chunks;
+    p.gran_shift = std::min(p.gran_shift, p.block_shift);
+    p.list_steps = static_cast<int>(
+        (static_cast<int64_t>(d->num_blocks) * d->block_size + dsa::kPaStep - 1) / dsa::kPaStep);
+    most_steps += p.list_steps;
   }
   p.scale_log2 = d->sm_scale * dsa::kPaLog2e;
-  p.q = static_cast<const uint16_t *>(q);
-  p.k = static_cast<const uint8_t *>(k);
-  p.v = static_cast<const uint8_t *>(v);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.sinks = sinks;
@@ -119,18 +136,33 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kWorkspaceHeader);
   p.part_ml = reinterpret_cast<float2 *>(p.part_o + part_floats());
   p.chain = reinterpret_cast<int4 *>(p.part_ml + static_cast<size_t>(kPaGrid) * 2 * dsa::kPaRows);
-  // no more CTAs than tiles
-  const int64_t most_tiles = std::max<int64_t>(1, (most_chunks + dsa::kPaWarps - 1) / dsa::kPaWarps);
-  const int64_t rows = static_cast<int64_t>(p.T) * p.g.H_kv * p.head_tiles;
-  const int grid = static_cast<int>(std::min<int64_t>(
-      std::min(kPaGrid, dev->num_sms * kPaCtasPerSm),
-      rows > kPaGrid ? rows : rows * most_tiles));
+  p.err = static_cast<unsigned int *>(workspace);
+  p.err_info = p.err + 1;
+  p.wait_limit_ns = d->wait_limit_ns ? d->wait_limit_ns : kPaWaitLimitNs;
+  p.drain_limit_ns = kPaDrainLimitNs;
+  CUtensorMap tq, tk, tv;
+  {
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(p.T) * p.H};
+    const cuuint64_t strides[1] = {256};
+    const cuuint32_t box[2] = {64, dsa::kPaRows};
+    st = make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, dims, strides, box);
+    if (st == DSA_OK) st = pool_map(&tk, &d->cache, k, 1 << p.gran_shift);
+    if (st == DSA_OK) st = pool_map(&tv, &d->cache, v, 1 << p.gran_shift);
+    if (st != DSA_OK) return st;
+  }
+  // no more CTAs than steps for their warps
+  const int64_t items = static_cast<int64_t>(p.T) * p.g.H_kv * p.head_tiles;
+  const int most = std::min(kPaGrid, dev->num_sms * kPaCtasPerSm);
+  const int64_t want = items > most * dsa::kPaWarps
+                           ? most
+                           : (items * std::max<int64_t>(1, most_steps) + dsa::kPaWarps - 1) / dsa::kPaWarps;
+  const int grid = static_cast<int>(std::min<int64_t>(most, want));
   const bool fp8 = d->cache.dtype != DSA_KV_BF16;
   if (list)
-    return fp8 ? launch<true, true>(p, grid, dev, kAttrPagedAttn + 3, stream)
-               : launch<false, true>(p, grid, dev, kAttrPagedAttn + 2, stream);
-  return fp8 ? launch<true, false>(p, grid, dev, kAttrPagedAttn + 1, stream)
-             : launch<false, false>(p, grid, dev, kAttrPagedAttn, stream);
+    return fp8 ? launch<true, true>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 3, stream)
+               : launch<false, true>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 2, stream);
+  return fp8 ? launch<true, false>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 1, stream)
+             : launch<false, false>(p, tq, tk, tv, grid, dev, kAttrPagedAttn, stream);
 }
 
 }  // namespace

@@ -21,7 +21,7 @@ dsa_status_t check_paged_cache(const dsa_paged_cache_t *c) {
   if (c->dtype != DSA_KV_BF16 && c->dtype != DSA_KV_FP8_E4M3_E8M0_B32) return DSA_ERR_INVALID_ARG;
   if (c->D != 128 || c->H_kv > 128) return DSA_ERR_UNSUPPORTED;
   for (const int64_t s : {c->page_stride, c->slot_stride, c->head_stride})
-    if (s < 0 || s % 128 != 0) return DSA_ERR_INVALID_ARG;
+    if (s < 128 || s % 128 != 0) return DSA_ERR_INVALID_ARG;
   if (!c->block_table || !aligned(c->block_table, 4)) return DSA_ERR_INVALID_ARG;
   // slots of a sequence and of the pool are 32-bit; a page's offset is 64-bit
   const int64_t ps = c->page_size;
@@ -168,10 +168,11 @@ dsa_status_t dsa_cache_append(const dsa_append_desc_t *desc, const void *q, cons
   const bool qf = desc->H > 0 ? q_fp8 : kv_fp8;
   const AppendFn fn = qf ? (kv_fp8 ? append_fn<true, true>(halves) : append_fn<true, false>(halves))
                          : (kv_fp8 ? append_fn<false, true>(halves) : append_fn<false, false>(halves));
-  constexpr int kUnitsPerBlock = dsa::kAppendThreads / dsa::kRowLanes;
-  const int64_t blocks =
-      (static_cast<int64_t>(p.T) * p.units + kUnitsPerBlock - 1) / kUnitsPerBlock;
-  if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const int lanes = qf || kv_fp8 ? dsa::kAppendLanes<true> : dsa::kAppendLanes<false>;
+  const int per_block = dsa::kAppendThreads / lanes;
+  const int64_t blocks = (static_cast<int64_t>(p.T) * p.units + per_block - 1) / per_block;
+  // the kernel numbers its threads in 32 bits
+  if (blocks * dsa::kAppendThreads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (launch_pdl(fn, static_cast<int>(blocks), dsa::kAppendThreads, 0,
                  reinterpret_cast<cudaStream_t>(stream), 0, p) != cudaSuccess)
     return DSA_ERR_CUDA;
@@ -198,13 +199,16 @@ dsa_status_t dsa_block_pool(const dsa_block_pool_desc_t *desc, const void *k_cac
   dsa::PoolParams p{};
   p.g = paged_geom(&c);
   p.block_size = desc->block_size;
-  // about kPoolBatch slots a half warp: each has one batch of loads to wait for
+  // 16 slots a half warp: the run it looks up at once
   p.share = 1;
-  while (p.share < dsa::kPoolRows && p.share * dsa::kPoolBatch < p.block_size) p.share *= 2;
-  const int per_cta = dsa::kPoolRows / p.share;
-  const int64_t most = (p.g.capacity() / p.block_size * c.H_kv + per_cta - 1) / per_cta;
-  const int64_t fill = std::max<int64_t>(1, static_cast<int64_t>(dev->num_sms) * 8 / c.num_seqs);
-  p.ctas_per_seq = static_cast<int>(std::max<int64_t>(1, std::min(most, fill)));
+  while (p.share < dsa::kPoolGroups && p.share * 16 < p.block_size) p.share *= 2;
+  p.together = std::max(1, 16 / p.block_size);
+  const int per_cta = dsa::kPoolGroups / p.share;
+  const int64_t sets = (p.g.capacity() / p.block_size + p.together - 1) / p.together;
+  // the kernel numbers up to kPoolSeqs sequences' items in 32 bits
+  if (sets * c.H_kv > INT32_MAX / std::min(c.num_seqs, dsa::kPoolSeqs)) return DSA_ERR_UNSUPPORTED;
+  const int64_t most = (sets * c.H_kv * c.num_seqs + per_cta - 1) / per_cta;
+  const int blocks = static_cast<int>(std::min<int64_t>(most, dev->num_sms * 3));   // one wave
   p.S_pool = desc->S_pool;
   p.seq_stride = desc->seq_stride;
   p.head_stride = desc->head_stride;
@@ -215,10 +219,8 @@ dsa_status_t dsa_block_pool(const dsa_block_pool_desc_t *desc, const void *k_cac
   p.pooled = pooled;
   p.pooled_scale = pooled_scale;
   p.last_block = last_block;
-  const int64_t blocks = static_cast<int64_t>(c.num_seqs) * p.ctas_per_seq;
-  if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   const auto fn = c.dtype == DSA_KV_BF16 ? dsa::block_pool_kernel<false> : dsa::block_pool_kernel<true>;
-  if (launch_pdl(fn, static_cast<int>(blocks), dsa::kPoolThreads, 0,
+  if (launch_pdl(fn, blocks, dsa::kPoolThreads, 0,
                  reinterpret_cast<cudaStream_t>(stream), 0, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   return DSA_OK;

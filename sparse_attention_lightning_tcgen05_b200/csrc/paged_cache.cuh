@@ -3,11 +3,11 @@
 // fp8), and the mean key of every completed block.
 //
 // Both move each byte once and compute next to nothing, so memory bounds the
-// long calls and the launch the short ones. A head row (128 features) is one
-// half warp's work: a lane holds 8 features, one 16-byte load, so that a
-// row is whole 128-byte lines; the rotation's partner features sit in the
-// same lane (interleaved pairs) or a fixed number of lanes away (halves), and
-// the 32 features of an e8m0 scale in four neighbouring lanes.
+// long calls and the launch the short ones; what they spend instructions on
+// is the fp8 format (a maximum, a scale and a conversion per feature). A head
+// row (128 features) lies across 8 or 16 neighbouring lanes: the rotation's
+// partner features sit in the same lane (interleaved pairs) or a fixed number
+// of lanes away (halves), and so do the 32 features of an e8m0 scale.
 #pragma once
 
 #include <cstdint>
@@ -19,7 +19,6 @@
 namespace dsa {
 
 constexpr int kRowD = 128;               // features of a head row
-constexpr int kRowLanes = 16;            // lanes a row
 
 struct PagedGeom {
   int num_seqs, H_kv;
@@ -85,34 +84,34 @@ __device__ __forceinline__ float e8m0_f32(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fffffffu : b << 23);
 }
 
-// A half warp's row in the block-32 fp8 format: 8 e4m3 bytes a lane and, in
-// every lane, the row's four scale bytes as one word. Called by whole warps.
-// 448 = 1.75 * 2^8, so the least e with amax <= 448 * 2^e is amax's exponent
-// less 8, plus one where its fraction is above .75: one integer addition to
-// amax's bits carries exactly then.
-__device__ __forceinline__ uint2 quantize_row(const float (&x)[8], uint32_t &scales) {
-  uint32_t top = 0;                       // magnitudes as integers: NaN > inf > numbers
+// The e8m0 byte of 32 features whose largest magnitude has the bits `top`, or
+// 255 where one is a NaN or an infinity (their bits compare above every
+// number's). 448 = 1.75 * 2^8, so the least e with amax <= 448 * 2^e is
+// amax's exponent less 8, plus one where its fraction is above .75: one integer
+// addition to amax's bits carries exactly then.
+__device__ __forceinline__ uint32_t e8m0_of(uint32_t top) {
+  return top < 0x7f800000u ? max(0, static_cast<int>((top + 0x1fffffu) >> 23) - 8) : 255;
+}
+
+// kN features (a multiple of 4) over 2^(e - 127) as e4m3 bytes; zeros for 255.
+template <int kN>
+__device__ __forceinline__ void quantize(const float (&x)[kN], uint32_t e, uint32_t (&out)[kN / 4]) {
+  // 2^(127 - e) by its exponent bits: e <= 247, so 254 - e >= 7
+  const float inv = __uint_as_float(e == 255 ? 0u : (254 - e) << 23);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const bool finite = top < 0x7f800000u;
-  const int e = max(0, static_cast<int>((top + 0x1fffffu) >> 23) - 8);   // e + 127
-  uint2 data = make_uint2(0u, 0u);
-  if (finite) {
-    // 2^-e by its exponent bits: e + 127 <= 247, so 254 - (e + 127) >= 7
-    const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
-    data.x = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
-    data.y = e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16;
+  for (int i = 0; i < kN / 4; ++i) {
+    const uint32_t w = e4m3x2(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv)) |
+                       e4m3x2(__fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv)) << 16;
+    out[i] = e == 255 ? 0u : w;
   }
-  uint32_t word = static_cast<uint32_t>(finite ? e : 255) << (8 * ((threadIdx.x >> 2) & 3));
-  word |= __shfl_xor_sync(0xffffffffu, word, 4);
-  word |= __shfl_xor_sync(0xffffffffu, word, 8);
-  scales = word;
-  return data;
+}
+
+template <int kN>
+__device__ __forceinline__ uint32_t largest_bits(const float (&x)[kN]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  return top;
 }
 
 // ---- append --------------------------------------------------------------------
@@ -131,135 +130,153 @@ struct AppendParams {
   uint8_t *q_scale, *k_scale, *v_scale;
 };
 
-constexpr int kAppendRows = 4;           // head rows a half warp holds at once
+constexpr int kAppendRows = 4;           // head rows a group of lanes holds at once
 constexpr int kAppendThreads = 256;
 
-// Writes one row (8 features a lane) at element offset `at` of a buffer.
+// Lanes of a head row: 16 of 8 features (a row's lines are read and written by
+// consecutive lanes) where rows stay bf16; eight of 16 where some become
+// fp8, whose per-row work (the scale, the address) then costs half.
 template <bool kFp8>
-__device__ __forceinline__ void store_row(const float (&x)[8], void *data, uint8_t *scale,
-                                          int64_t at, int l, bool write) {
-  if constexpr (kFp8) {
-    uint32_t scales;
-    const uint2 d = quantize_row(x, scales);
-    if (write) {
-      *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(data) + at + 8 * l) = d;
-      if (l == 0) *reinterpret_cast<uint32_t *>(scale + at / 32) = scales;
-    }
-  } else {
-    if (write)
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(data) + at + 8 * l) = pack8(x);
-  }
-}
+constexpr int kAppendLanes = kFp8 ? 8 : 16;
 
-// A half warp takes kAppendRows head rows of one token, whose cosines and
+// A group of lanes takes kAppendRows head rows of one token, whose cosines and
 // sines it reads once. Products and sums of the rotation are rounded one by
 // one (no fma), so that the result is the formula's in fp32.
 template <bool kQFp8, bool kKvFp8, bool kHalves>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
+  constexpr int kLanes = kAppendLanes<kQFp8 || kKvFp8>;
+  constexpr int kF = kRowD / kLanes, kP = kF / 8;    // a lane's features, its 8-feature pieces
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int l = threadIdx.x & (kRowLanes - 1);
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x) / kRowLanes;
-  int t = static_cast<int>(unit / p.units);
-  const int r0 = static_cast<int>(unit - static_cast<int64_t>(t) * p.units) * kAppendRows;
+  const int l = threadIdx.x & (kLanes - 1);
+  const uint32_t unit = (blockIdx.x * kAppendThreads + threadIdx.x) / kLanes;
+  int t = static_cast<int>(unit / static_cast<uint32_t>(p.units));
+  const int r0 = static_cast<int>(unit - static_cast<uint32_t>(t) * p.units) * kAppendRows;
   const bool in = t < p.T;
   if (!in) t = 0;
   const int pos = __ldg(p.positions + t);
   const bool live = in && pos >= 0;
+  const int kv0 = p.H, v0 = p.H + p.g.H_kv;          // first key row, first value row
 
-  uint4 raw[kAppendRows];
+  uint4 raw[kAppendRows][kP];
 #pragma unroll
   for (int i = 0; i < kAppendRows; ++i) {
     const int r = r0 + i;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int u = 0; u < kP; ++u) raw[i][u] = make_uint4(0u, 0u, 0u, 0u);
     if (live && r < p.rows) {
-      const uint16_t *src;
-      if (r < p.H) src = p.q + t * p.q_stride + static_cast<int64_t>(r) * kRowD;
-      else if (r < p.H + p.g.H_kv) src = p.k + t * p.k_stride + static_cast<int64_t>(r - p.H) * kRowD;
-      else src = p.v + t * p.v_stride + static_cast<int64_t>(r - p.H - p.g.H_kv) * kRowD;
-      raw[i] = *reinterpret_cast<const uint4 *>(src + 8 * l);
+      const uint16_t *src = r < kv0  ? p.q + t * p.q_stride + r * kRowD
+                            : r < v0 ? p.k + t * p.k_stride + (r - kv0) * kRowD
+                                     : p.v + t * p.v_stride + (r - v0) * kRowD;
+#pragma unroll
+      for (int u = 0; u < kP; ++u) raw[i][u] = reinterpret_cast<const uint4 *>(src)[kP * l + u];
     }
   }
   // the token's slot
   int64_t slot = -1;
-  if (live && r0 + kAppendRows > p.H) {
+  if (live && r0 + kAppendRows > kv0) {
     const int seq = p.seq_ids ? __ldg(p.seq_ids + t) : t;
     if (seq >= 0 && seq < p.g.num_seqs && pos < p.g.capacity()) slot = paged_slot(p.g, seq, pos);
   }
-  // this lane's cosines and sines
+  // cosines and sines of this lane's pieces: eight (halves) or four (pairs) each
   constexpr int kC = kHalves ? 8 : 4;
-  const int c0 = kHalves ? (8 * l < p.half ? 8 * l : 8 * l - p.half) : 4 * l;
-  const bool turn = 8 * l < 2 * p.half;
-  float c[kC], s[kC];
+  float c[kP][kC], s[kP][kC];
 #pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
-  }
-  if (turn && live && r0 < p.H + p.g.H_kv) {
-    const float *cr = p.cos + static_cast<int64_t>(t) * p.half + c0;
-    const float *sr = p.sin + static_cast<int64_t>(t) * p.half + c0;
-    if (p.vec) {
+  for (int u = 0; u < kP; ++u) {
+    const int f = 8 * (kP * l + u);                   // the piece's first feature
+    const int c0 = kHalves ? (f < p.half ? f : f - p.half) : f / 2;
 #pragma unroll
-      for (int i = 0; i < kC; i += 4) {
-        *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(cr + i);
-        *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(sr + i);
-      }
-    } else {
+    for (int i = 0; i < kC; ++i) {
+      c[u][i] = 1.f;
+      s[u][i] = 0.f;
+    }
+    if (f < 2 * p.half && live && r0 < v0) {
+      const float *cr = p.cos + static_cast<int64_t>(t) * p.half + c0;
+      const float *sr = p.sin + static_cast<int64_t>(t) * p.half + c0;
+      if (p.vec) {
 #pragma unroll
-      for (int i = 0; i < kC; ++i)
-        if (c0 + i < p.half) {
-          c[i] = cr[i];
-          s[i] = sr[i];
+        for (int i = 0; i < kC; i += 4) {
+          *reinterpret_cast<float4 *>(&c[u][i]) = *reinterpret_cast<const float4 *>(cr + i);
+          *reinterpret_cast<float4 *>(&s[u][i]) = *reinterpret_cast<const float4 *>(sr + i);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+          if (c0 + i < p.half) {
+            c[u][i] = cr[i];
+            s[u][i] = sr[i];
+          }
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < kAppendRows; ++i) {
     const int r = r0 + i;
-    float x[8];
-    unpack8(raw[i], x);
+    float x[kF];
+#pragma unroll
+    for (int u = 0; u < kP; ++u) unpack8(raw[i][u], *reinterpret_cast<float (*)[8]>(&x[8 * u]));
     if constexpr (kHalves) {
-      // features j and j + half sit half / 8 lanes apart
+      // features j and j + half sit half / 8 pieces apart: in the lane that
+      // holds that piece, as its same or (two pieces a lane, half / 8 odd) its
+      // other one
       const int apart = p.half / 8;
-      const bool low = 8 * l < p.half;
-      const int from = turn ? (low ? l + apart : l - apart) : l;
-      uint4 o;
-      o.x = __shfl_sync(0xffffffffu, raw[i].x, from, kRowLanes);
-      o.y = __shfl_sync(0xffffffffu, raw[i].y, from, kRowLanes);
-      o.z = __shfl_sync(0xffffffffu, raw[i].z, from, kRowLanes);
-      o.w = __shfl_sync(0xffffffffu, raw[i].w, from, kRowLanes);
-      if (turn && r < p.H + p.g.H_kv) {
-        float y[8];
-        unpack8(o, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = low ? __fsub_rn(__fmul_rn(x[j], c[j]), __fmul_rn(y[j], s[j]))
-                     : __fadd_rn(__fmul_rn(y[j], s[j]), __fmul_rn(x[j], c[j]));
+      for (int u = 0; u < kP; ++u) {
+        const int piece = kP * l + u;
+        const bool low = piece < apart, turn = piece < 2 * apart;
+        const int from = (turn ? (low ? piece + apart : piece - apart) : piece) / kP;
+        const uint4 give = kP == 2 && (apart & 1) ? raw[i][kP - 1 - u] : raw[i][u];
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, give.x, from, kLanes);
+        o.y = __shfl_sync(0xffffffffu, give.y, from, kLanes);
+        o.z = __shfl_sync(0xffffffffu, give.z, from, kLanes);
+        o.w = __shfl_sync(0xffffffffu, give.w, from, kLanes);
+        if (turn && r < v0) {
+          float y[8];
+          unpack8(o, y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float a = x[8 * u + j];
+            x[8 * u + j] = low ? __fsub_rn(__fmul_rn(a, c[u][j]), __fmul_rn(y[j], s[u][j]))
+                               : __fadd_rn(__fmul_rn(y[j], s[u][j]), __fmul_rn(a, c[u][j]));
+          }
+        }
       }
-    } else if (turn && r < p.H + p.g.H_kv) {
+    } else if (kF * l < 2 * p.half && r < v0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * l + j < p.half) {
+      for (int j = 0; j < kF / 2; ++j)
+        if (kF / 2 * l + j < p.half) {
           const float a = x[2 * j], b = x[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(a, c[j]), __fmul_rn(b, s[j]));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(a, s[j]), __fmul_rn(b, c[j]));
+          x[2 * j] = __fsub_rn(__fmul_rn(a, c[j >> 2][j & 3]), __fmul_rn(b, s[j >> 2][j & 3]));
+          x[2 * j + 1] = __fadd_rn(__fmul_rn(a, s[j >> 2][j & 3]), __fmul_rn(b, c[j >> 2][j & 3]));
         }
     }
-    // r is the same in both half warps only by chance: the branch below does
-    // not hold the warp-wide shuffles of the fp8 rows
-    const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.g.H_kv;
-    const int64_t q_at = (static_cast<int64_t>(t) * p.H + r) * kRowD;
-    if constexpr (kQFp8 == kKvFp8) {
-      const int64_t at = is_q ? q_at : slot + (is_k ? r - p.H : r - p.H - p.g.H_kv) * p.g.head_stride;
-      store_row<kQFp8>(x, is_q ? p.q_out : is_k ? p.k_cache : p.v_cache,
-                       is_q ? p.q_scale : is_k ? p.k_scale : p.v_scale, at, l,
-                       live && r < p.rows && (is_q || slot >= 0));
-    } else {
-      store_row<kQFp8>(x, p.q_out, p.q_scale, q_at, l, live && is_q);
-      store_row<kKvFp8>(x, is_k ? p.k_cache : p.v_cache, is_k ? p.k_scale : p.v_scale,
-                        slot + (is_k ? r - p.H : r - p.H - p.g.H_kv) * p.g.head_stride, l,
-                        live && !is_q && r < p.rows && slot >= 0);
+    // where the row goes (the fp8 rows' shuffles below are the whole warp's)
+    const bool is_q = r < kv0, is_k = !is_q && r < v0;
+    const bool write = live && r < p.rows && (is_q || slot >= 0);
+    const int64_t at = is_q ? (static_cast<int64_t>(t) * p.H + r) * kRowD
+                            : slot + (is_k ? r - kv0 : r - v0) * p.g.head_stride;
+    void *const data = is_q ? p.q_out : is_k ? p.k_cache : p.v_cache;
+    if constexpr (kQFp8 || kKvFp8) {
+      uint32_t top = largest_bits(x);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      const uint32_t e = e8m0_of(top);
+      uint32_t word = e << (8 * (l >> 1));           // the row's four scales
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      if (write && (is_q ? kQFp8 : kKvFp8)) {
+        uint32_t d[4];
+        quantize(x, e, d);
+        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(data) + at + 16 * l) =
+            make_uint4(d[0], d[1], d[2], d[3]);
+        uint8_t *const scale = is_q ? p.q_scale : is_k ? p.k_scale : p.v_scale;
+        if (l == 0) *reinterpret_cast<uint32_t *>(scale + at / 32) = word;
+      }
+    }
+    if (!(kQFp8 && kKvFp8) && write && !(is_q ? kQFp8 : kKvFp8)) {
+      uint4 *const dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(data) + at) + kP * l;
+#pragma unroll
+      for (int u = 0; u < kP; ++u) dst[u] = pack8(*reinterpret_cast<const float (*)[8]>(&x[8 * u]));
     }
   }
 }
@@ -269,8 +286,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 struct PoolParams {
   PagedGeom g;
   int block_size;
-  int share;                 // half warps a pooled row (1 .. kPoolRows, a power of two)
-  int ctas_per_seq;
+  int share;                 // half warps a pooled row (1 .. kPoolGroups, a power of two)
+  int together;              // pooled rows a half warp sums at once (1 where share > 1)
   int64_t S_pool, seq_stride, head_stride;
   const void *k;
   const uint8_t *k_scale;
@@ -281,104 +298,214 @@ struct PoolParams {
 };
 
 constexpr int kPoolThreads = 256;
-constexpr int kPoolRows = kPoolThreads / kRowLanes;
-constexpr int kPoolBatch = 4;            // key rows a half warp has in flight
+constexpr int kPoolLanes = 16;           // lanes a key row, 8 features each
+constexpr int kPoolGroups = kPoolThreads / kPoolLanes;
+constexpr int kPoolBatch = 8;            // key rows a half warp has in flight
 
-// ctas_per_seq CTAs walk a sequence's fresh (block, head) rows; `share` half
-// warps sum a row's slots and the first of them joins their sums (in order,
-// so that the result does not depend on timing) and writes it.
+// One pooled row, 8 features a lane; called by whole warps.
+template <bool kFp8>
+__device__ __forceinline__ void pool_store(const float (&x)[8], const PoolParams &p, int seq,
+                                           int h, int b, int l, bool write) {
+  const int64_t at = seq * p.seq_stride + h * p.head_stride + static_cast<int64_t>(b) * kRowD;
+  if constexpr (kFp8) {
+    uint32_t top = largest_bits(x);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t e = e8m0_of(top);
+    uint32_t word = e << (8 * (l >> 2));
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    if (write) {
+      uint32_t d[2];
+      quantize(x, e, d);
+      reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.pooled) + at)[l] = make_uint2(d[0], d[1]);
+      if (l == 0) *reinterpret_cast<uint32_t *>(p.pooled_scale + at / 32) = word;
+    }
+  } else {
+    if (write) reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.pooled) + at)[l] = pack8(x);
+  }
+}
+
+constexpr int kPoolSeqs = 1024;          // sequences the CTAs share out at once
+
+// First fresh block of a sequence, and one past the last.
+__device__ __forceinline__ int2 pool_range(const PoolParams &p, int seq, int &done) {
+  const int cap = static_cast<int>(p.g.capacity());
+  const int pos = __ldg(p.positions + seq);
+  const int n = pos < cap ? pos + 1 : cap;                  // slots held
+  done = n > 0 ? n / p.block_size : 0;
+  const int first = p.start ? max(0, __ldg(p.start + seq)) / p.block_size : 0;
+  return make_int2(first, static_cast<int>(min(static_cast<int64_t>(done), p.S_pool)));
+}
+
+// All sequences' fresh blocks (runs of `together` blocks of a head: the items)
+// are counted by every CTA, which then takes an equal share of them, so that
+// sequences of any lengths fill the GPU evenly. A half warp looks 16 slots up
+// at once (a lane each) and reads their rows in batches of eight: the slots of
+// `together` small blocks, or a run of a large block that `share` half warps
+// sum; the first of those joins the sums (in order, so that the result does
+// not depend on timing) and writes the row.
 template <bool kFp8>
 __global__ void __launch_bounds__(kPoolThreads) block_pool_kernel(const PoolParams p) {
-  __shared__ float part[kPoolRows][kRowD];
+  __shared__ float part[kPoolGroups][kRowD];
+  __shared__ uint32_t ends[kPoolSeqs];                      // items up to and with a sequence's
+  __shared__ uint32_t warp_sum[kPoolThreads / 32];
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int seq = blockIdx.x / p.ctas_per_seq;
-  const int cta = blockIdx.x - seq * p.ctas_per_seq;
-  const int l = threadIdx.x & (kRowLanes - 1), grp = threadIdx.x / kRowLanes;
-  const int64_t cap = p.g.capacity();
-  const int64_t n = min(static_cast<int64_t>(__ldg(p.positions + seq)) + 1, cap);   // slots held
-  const int64_t done = n > 0 ? n / p.block_size : 0;
-  if (p.last_block && cta == 0)
-    for (int h = threadIdx.x; h < p.g.H_kv; h += kPoolThreads)
-      p.last_block[static_cast<int64_t>(seq) * p.g.H_kv + h] = static_cast<int>(done) - 1;
-  const int64_t first = p.start ? max(0, __ldg(p.start + seq)) / p.block_size : 0;
-  const int64_t items = (min(done, p.S_pool) - first) * p.g.H_kv;
-  const int per_cta = kPoolRows / p.share;
-  const int row = grp / p.share, part_of = grp - row * p.share;
-  for (int64_t it0 = static_cast<int64_t>(cta) * per_cta; it0 < items;
-       it0 += static_cast<int64_t>(p.ctas_per_seq) * per_cta) {
-    const int64_t it = it0 + row;
-    const bool in = it < items;
-    const int64_t b = first + (in ? it / p.g.H_kv : 0);
-    const int h = in ? static_cast<int>(it % p.g.H_kv) : 0;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      const int s0 = static_cast<int>(b * p.block_size);
-      for (int j0 = part_of; j0 < p.block_size; j0 += p.share * kPoolBatch) {
-        int64_t at[kPoolBatch];
+  const int l = threadIdx.x & (kPoolLanes - 1), grp = threadIdx.x / kPoolLanes;
+  const int per_cta = kPoolGroups / p.share;
+  const int mine = grp / p.share, part_of = grp - mine * p.share;
+  const float size = static_cast<float>(p.block_size);
+  for (int seq0 = 0; seq0 < p.g.num_seqs; seq0 += kPoolSeqs) {
+    const int seqs = min(kPoolSeqs, p.g.num_seqs - seq0);
+    // ---- items of each sequence, summed up: four sequences a thread ----
+    constexpr int kEach = kPoolSeqs / kPoolThreads;
+    uint32_t count[kEach], sum = 0;
 #pragma unroll
-        for (int u = 0; u < kPoolBatch; ++u) {
-          const int j = j0 + u * p.share;
-          at[u] = j < p.block_size ? paged_slot(p.g, seq, s0 + j) : -1;
-        }
-        if constexpr (kFp8) {
-          uint2 w[kPoolBatch];
-          uint32_t sc[kPoolBatch];
+    for (int i = 0; i < kEach; ++i) {
+      const int s = threadIdx.x * kEach + i;
+      int done = 0;
+      count[i] = 0;
+      if (s < seqs) {
+        const int2 r = pool_range(p, seq0 + s, done);
+        if (r.y > r.x) count[i] = static_cast<uint32_t>((r.y - r.x + p.together - 1) / p.together) * p.g.H_kv;
+        if (p.last_block && blockIdx.x == 0)
+          for (int h = 0; h < p.g.H_kv; ++h)
+            p.last_block[static_cast<int64_t>(seq0 + s) * p.g.H_kv + h] = done - 1;
+      }
+      sum += count[i];
+    }
+    uint32_t incl = sum;
 #pragma unroll
-          for (int u = 0; u < kPoolBatch; ++u) {
-            w[u] = make_uint2(0u, 0u);
-            sc[u] = 127;
-            if (at[u] >= 0) {
-              const int64_t o = at[u] + h * p.g.head_stride;
-              w[u] = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.k) + o + 8 * l);
-              sc[u] = p.k_scale[o / 32 + l / 4];
-            }
-          }
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+      if ((threadIdx.x & 31) >= off) incl += o;
+    }
+    __syncthreads();                                          // the last turn's readers are done
+    if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = incl;
+    __syncthreads();
+    uint32_t items = 0, at0 = incl - sum;
 #pragma unroll
-          for (int u = 0; u < kPoolBatch; ++u) {
-            const float f = e8m0_f32(sc[u]);
-            const uint32_t q[4] = {w[u].x & 0xffffu, w[u].x >> 16, w[u].y & 0xffffu, w[u].y >> 16};
+    for (int w = 0; w < kPoolThreads / 32; ++w) {
+      if (w < threadIdx.x >> 5) at0 += warp_sum[w];
+      items += warp_sum[w];
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 v = e4m3x2_f32(q[i]);
-              acc[2 * i] += v.x * f;
-              acc[2 * i + 1] += v.y * f;
-            }
-          }
-        } else {
+    for (int i = 0; i < kEach; ++i) ends[threadIdx.x * kEach + i] = at0 += count[i];
+    __syncthreads();
+    // ---- this CTA's share, in turns of per_cta items ----
+    const uint32_t turns_all = (items + per_cta - 1) / per_cta;
+    const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(turns_all) * blockIdx.x / gridDim.x) * per_cta;
+    const uint32_t end = min(items, static_cast<uint32_t>(static_cast<uint64_t>(turns_all) * (blockIdx.x + 1) /
+                                                         gridDim.x) * per_cta);
+    int s = 0;
+    {
+      // the sequence of this half warp's first item
+      int hi = seqs - 1;
+      while (s < hi) {
+        const int mid = (s + hi) / 2;
+        if (begin + mine < ends[mid]) hi = mid;
+        else s = mid + 1;
+      }
+    }
+    for (uint32_t it0 = begin; it0 < end; it0 += per_cta) {
+      const uint32_t it = it0 + mine;
+      const bool in = it < end;
+      while (in && it >= ends[s]) ++s;
+      const int seq = seq0 + s;
+      int done;
+      const int2 range = pool_range(p, seq, done);
+      const uint32_t local = in ? it - (s > 0 ? ends[s - 1] : 0) : 0;
+      const uint32_t set = local / static_cast<uint32_t>(p.g.H_kv);
+      const int h = static_cast<int>(local - set * p.g.H_kv);
+      const int b0 = range.x + static_cast<int>(set) * p.together;
+      const int blocks = in ? min(p.together, range.y - b0) : 0;
+      const int slot0 = b0 * p.block_size;
+      const int slots = blocks * p.block_size;                       // of this half warp's set
+      const int64_t head_off = h * p.g.head_stride;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      int left = p.block_size, b = b0;                               // slots until the block ends
+      // a run of 16 slots a time; every lane of the warp takes as many turns
+      const int turns = (p.together * p.block_size + 16 * p.share - 1) / (16 * p.share);
+      for (int turn = 0; turn < turns; ++turn) {
+        const int j0 = (turn * p.share + part_of) * 16;
+        int64_t at = -1;
+        uint32_t sc = 0x7f7f7f7fu;
+        if (j0 + l < slots) at = paged_slot(p.g, seq, slot0 + j0 + l);
+        if (at >= 0) at += head_off;
+        if (kFp8 && at >= 0) sc = __ldg(reinterpret_cast<const uint32_t *>(p.k_scale + at / 32));
+#pragma unroll
+        for (int j1 = 0; j1 < 16; j1 += kPoolBatch) {
+          if (j1 >= p.together * p.block_size) break;                // the same for all lanes
           uint4 w[kPoolBatch];
+          uint32_t f[kPoolBatch];
 #pragma unroll
           for (int u = 0; u < kPoolBatch; ++u) {
+            const int64_t a = __shfl_sync(0xffffffffu, at, j1 + u, kPoolLanes);
             w[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (at[u] >= 0)
-              w[u] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + at[u] +
-                                                      h * p.g.head_stride + 8 * l);
+            if constexpr (kFp8) {
+              f[u] = __shfl_sync(0xffffffffu, sc, j1 + u, kPoolLanes) >> (8 * (l >> 2)) & 0xffu;
+              if (a >= 0) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.k) + a) + l);
+                w[u].x = v.x;
+                w[u].y = v.y;
+              }
+            } else {
+              if (a >= 0)
+                w[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + a) + l);
+            }
           }
 #pragma unroll
           for (int u = 0; u < kPoolBatch; ++u) {
-            float v[8];
-            unpack8(w[u], v);
+            if constexpr (kFp8) {
+              const float e = e8m0_f32(f[u]);
+              const uint32_t q[4] = {w[u].x & 0xffffu, w[u].x >> 16, w[u].y & 0xffffu, w[u].y >> 16};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += v[i];
+              for (int i = 0; i < 4; ++i) {
+                const float2 v = e4m3x2_f32(q[i]);
+                acc[2 * i] = fmaf(v.x, e, acc[2 * i]);
+                acc[2 * i + 1] = fmaf(v.y, e, acc[2 * i + 1]);
+              }
+            } else {
+              float v[8];
+              unpack8(w[u], v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) acc[i] += v[i];
+            }
+            if (p.share == 1) {
+              // a block ends: write its mean and start over
+              const bool end = --left == 0;
+              if (__any_sync(0xffffffffu, end)) {
+                if (end) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) acc[i] = __fdiv_rn(acc[i], size);
+                }
+                pool_store<kFp8>(acc, p, seq, h, b, l, end && b - b0 < blocks);
+                if (end) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+                  left = p.block_size;
+                  ++b;
+                }
+              }
+            }
           }
         }
       }
+      if (p.share > 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[grp][8 * l + i] = acc[i];
+        __syncthreads();
+        if (part_of == 0)
+          for (int u = 1; u < p.share; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += part[grp + u][8 * l + i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __fdiv_rn(acc[i], size);
+        pool_store<kFp8>(acc, p, seq, h, b0, l, in && part_of == 0);
+      }
     }
-    if (p.share > 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) part[grp][8 * l + i] = acc[i];
-      __syncthreads();
-      if (part_of == 0)
-        for (int u = 1; u < p.share; ++u)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += part[grp + u][8 * l + i];
-      __syncthreads();
-    }
-    const float size = static_cast<float>(p.block_size);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = __fdiv_rn(acc[i], size);
-    store_row<kFp8>(acc, p.pooled, p.pooled_scale,
-                    seq * p.seq_stride + h * p.head_stride + b * kRowD, l, in && part_of == 0);
   }
 }
 
