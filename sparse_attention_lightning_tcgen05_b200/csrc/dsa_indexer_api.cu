@@ -195,12 +195,11 @@ int64_t workspace_scores(void *ws, size_t ws_bytes, float **scores) {
 
 dsa_status_t make_map(CUtensorMap *m, CUtensorMapDataType dt, cuuint32_t rank, const void *base,
                       const cuuint64_t *dims, const cuuint64_t *strides_bytes,
-                      const cuuint32_t *box, CUtensorMapSwizzle swz) {
-  cuuint32_t estr[4] = {1, 1, 1, 1};
+                      const cuuint32_t *box, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2) {
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = g_encode(m, dt, rank, const_cast<void *>(base), dims, strides_bytes, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_INVALID_ARG;
 }
 

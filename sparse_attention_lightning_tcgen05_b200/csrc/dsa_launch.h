@@ -49,7 +49,8 @@ dsa_status_t ensure_smem_attr(DeviceInfo *d, uint32_t bit, K kernel, int bytes) 
 dsa_status_t make_map(CUtensorMap *m, CUtensorMapDataType dt, cuuint32_t rank, const void *base,
                       const cuuint64_t *dims, const cuuint64_t *strides_bytes,
                       const cuuint32_t *box,
-                      CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
+                      CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B,
+                      CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 inline bool aligned(const void *p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;

@@ -68,19 +68,25 @@ dsa_status_t launch(const dsa::PagedAttnParams &p, const CUtensorMap &tq, const 
   return DSA_OK;
 }
 
-// A pool [num_pages][H_kv][page_size] of rows of 128, boxes of `rows` slots and
-// 128 bytes.
-dsa_status_t pool_map(CUtensorMap *m, const dsa_paged_cache_t *c, const void *base, int rows) {
+// A pool as [page][head][half of a row][slot][128 bytes] (an fp8 row is one
+// half), in boxes of `rows` slots: both halves of them where they are a whole
+// stage of the kernel (`both`), one after the other in shared memory.
+dsa_status_t pool_map(CUtensorMap *m, const dsa_paged_cache_t *c, const void *base, int rows,
+                      bool both) {
   const bool fp8 = c->dtype != DSA_KV_BF16;
-  const cuuint64_t elt = fp8 ? 1 : 2;
-  const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(c->page_size),
+  const cuuint64_t elt = fp8 ? 1 : 2, halves = fp8 ? 1 : 2;
+  const cuuint64_t dims[5] = {128 / halves, static_cast<cuuint64_t>(c->page_size), halves,
                               static_cast<cuuint64_t>(c->H_kv), static_cast<cuuint64_t>(c->num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->slot_stride) * elt,
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(c->slot_stride) * elt, 128,
                                  static_cast<cuuint64_t>(c->head_stride) * elt,
                                  static_cast<cuuint64_t>(c->page_stride) * elt};
-  const cuuint32_t box[4] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(rows), 1, 1};
-  return make_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base,
-                  dims, strides, box);
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(dims[0]), static_cast<cuuint32_t>(rows),
+                             both ? static_cast<cuuint32_t>(halves) : 1, 1, 1};
+  // no more of a line than the box's 128 bytes of an fp8 row: the next 128 are
+  // another head's
+  return make_map(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base,
+                  dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                  fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *q, const void *k,
@@ -104,24 +110,30 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   st = device_info(&dev);
   if (st != DSA_OK) return st;
 
+  const bool fp8 = d->cache.dtype != DSA_KV_BF16;
   dsa::PagedAttnParams p{};
   p.g = paged_geom(&d->cache);
   p.T = d->T;
   p.H = d->H;
   p.G = d->H / d->cache.H_kv;
-  p.head_tiles = (p.G + dsa::kPaRows - 1) / dsa::kPaRows;
+  p.rows = dsa::kPaRows;
+  p.head_tiles = (p.G + p.rows - 1) / p.rows;
   p.window = d->window;
-  p.gran_shift = std::min(5, p.g.page_shift);
-  int64_t most_steps = (p.g.capacity() + dsa::kPaStep - 1) / dsa::kPaStep;
+  // tokens that share a sequence read the same slots: head by head, so that one
+  // head's slots stay in L2 while all its tokens pass
+  p.head_major = p.T > p.g.num_seqs;
+  const int step = fp8 ? dsa::PaSmem<true>::kStep : dsa::PaSmem<false>::kStep;
+  p.gran_shift = std::min(fp8 ? 5 : 4, p.g.page_shift);            // a step at most
+  int64_t most_steps = (p.g.capacity() + step - 1) / step;
   if (d->window > 0 || list)       // a window may begin inside a step
-    most_steps = std::min<int64_t>(most_steps, d->window / dsa::kPaStep + 2);
+    most_steps = std::min<int64_t>(most_steps, (d->window + 31) / step + 2);
   if (list) {
     p.block_shift = __builtin_ctz(static_cast<unsigned>(d->block_size));
     p.num_blocks = d->num_blocks;
     p.block_heads = d->block_heads;
     p.gran_shift = std::min(p.gran_shift, p.block_shift);
     p.list_steps = static_cast<int>(
-        (static_cast<int64_t>(d->num_blocks) * d->block_size + dsa::kPaStep - 1) / dsa::kPaStep);
+        (static_cast<int64_t>(d->num_blocks) * d->block_size + step - 1) / step);
     most_steps += p.list_steps;
   }
   p.scale_log2 = d->sm_scale * dsa::kPaLog2e;
@@ -146,18 +158,17 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
     const cuuint64_t strides[1] = {256};
     const cuuint32_t box[2] = {64, dsa::kPaRows};
     st = make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, dims, strides, box);
-    if (st == DSA_OK) st = pool_map(&tk, &d->cache, k, 1 << p.gran_shift);
-    if (st == DSA_OK) st = pool_map(&tv, &d->cache, v, 1 << p.gran_shift);
+    if (st == DSA_OK) st = pool_map(&tk, &d->cache, k, 1 << p.gran_shift, 1 << p.gran_shift == step);
+    if (st == DSA_OK) st = pool_map(&tv, &d->cache, v, 1 << p.gran_shift, 1 << p.gran_shift == step);
     if (st != DSA_OK) return st;
   }
   // no more CTAs than steps for their warps
   const int64_t items = static_cast<int64_t>(p.T) * p.g.H_kv * p.head_tiles;
   const int most = std::min(kPaGrid, dev->num_sms * kPaCtasPerSm);
-  const int64_t want = items > most * dsa::kPaWarps
+  const int64_t want = items > most * dsa::kPaWarps * 2
                            ? most
-                           : (items * std::max<int64_t>(1, most_steps) + dsa::kPaWarps - 1) / dsa::kPaWarps;
+                           : (items * std::max<int64_t>(1, most_steps) + 2 * dsa::kPaWarps - 1) / (2 * dsa::kPaWarps);
   const int grid = static_cast<int>(std::min<int64_t>(most, want));
-  const bool fp8 = d->cache.dtype != DSA_KV_BF16;
   if (list)
     return fp8 ? launch<true, true>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 3, stream)
                : launch<false, true>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 2, stream);
