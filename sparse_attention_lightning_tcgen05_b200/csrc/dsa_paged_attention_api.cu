@@ -11,6 +11,7 @@
 #include "dsa_launch.h"
 #include "dsa_paged_attention.h"
 #include "paged_attention.cuh"
+#include "paged_attention_wide.cuh"
 #include "paged_geom.h"
 
 namespace dsa_host {
@@ -19,7 +20,7 @@ namespace {
 // The partial results' room is sized for the 148 SMs of a B200, so that the
 // workspace size depends on the descriptor alone.
 constexpr int kPaCtasPerSm = 2;
-constexpr int kPaGrid = 148 * kPaCtasPerSm;
+constexpr int kSizingSms = 148;
 constexpr uint64_t kPaWaitLimitNs = 4000000000ull;
 constexpr uint64_t kPaDrainLimitNs = 4000000000ull;
 
@@ -46,27 +47,33 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
   return DSA_OK;
 }
 
-size_t part_floats() { return static_cast<size_t>(kPaGrid) * 2 * dsa::kPaRows * dsa::kRowD; }
+// The kernel of a call. Wide: more than 16 heads a key-value head of a bf16
+// cache, which would otherwise read every slot more than once.
+struct Plan {
+  bool fp8, wide;
+  int rows, head_tiles, step, grid;      // grid: CTAs at most
+};
 
-size_t workspace_bytes_needed() {
-  return kWorkspaceHeader + part_floats() * 4 + static_cast<size_t>(kPaGrid) * 2 * dsa::kPaRows * 8 +
-         static_cast<size_t>(kPaGrid) * 16;
+Plan plan_of(const dsa_paged_attention_desc_t *d) {
+  Plan p{};
+  const int G = d->H / d->cache.H_kv;
+  p.fp8 = d->cache.dtype != DSA_KV_BF16;
+  p.wide = !p.fp8 && G > dsa::kPaRows;
+  p.rows = p.wide ? dsa::kPwRows : dsa::kPaRows;
+  p.head_tiles = (G + p.rows - 1) / p.rows;
+  p.step = p.wide ? dsa::kPwTile : p.fp8 ? dsa::PaSmem<true>::kStep : dsa::PaSmem<false>::kStep;
+  p.grid = p.wide ? kSizingSms : kSizingSms * kPaCtasPerSm;
+  return p;
 }
 
-template <bool kFp8, bool kList>
-dsa_status_t launch(const dsa::PagedAttnParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                    const CUtensorMap &tv, int grid, DeviceInfo *dev, uint32_t bit, cudaStream_t s) {
-  const int smem = dsa::PaSmem<kFp8>::kTotal;
-  const dsa_status_t st = ensure_smem_attr(dev, bit, dsa::paged_attention_kernel<kFp8, kList>, smem);
-  if (st != DSA_OK) return st;
-  if (launch_pdl(dsa::paged_attention_kernel<kFp8, kList>, grid, dsa::kPaThreads,
-                 static_cast<size_t>(smem), s, 0, tq, tk, tv, p) != cudaSuccess)
-    return DSA_ERR_CUDA;
-  if (launch_pdl(dsa::paged_attention_join_kernel, grid * (dsa::kPaRows / 2), dsa::kPaJoinThreads, 0,
-                 s, 0, p) != cudaSuccess)
-    return DSA_ERR_CUDA;
-  return DSA_OK;
+size_t part_rows(const Plan &p) { return static_cast<size_t>(p.grid) * 2 * p.rows; }
+
+size_t workspace_bytes_needed(const Plan &p) {
+  return kWorkspaceHeader + part_rows(p) * (dsa::kRowD * 4 + 8) + static_cast<size_t>(p.grid) * 16;
 }
+
+using AttnFn = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                        const dsa::PagedAttnParams);
 
 // A pool as [page][head][half of a row][slot][128 bytes] (an fp8 row is one
 // half), in boxes of `rows` slots: both halves of them where they are a whole
@@ -104,36 +111,37 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   if (st != DSA_OK) return st;
   st = check_pool(&d->cache, v, v_scale);
   if (st != DSA_OK) return st;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_bytes_needed())
+  const Plan plan = plan_of(d);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_bytes_needed(plan))
     return DSA_ERR_WORKSPACE;
   DeviceInfo *dev = nullptr;
   st = device_info(&dev);
   if (st != DSA_OK) return st;
 
-  const bool fp8 = d->cache.dtype != DSA_KV_BF16;
   dsa::PagedAttnParams p{};
   p.g = paged_geom(&d->cache);
   p.T = d->T;
   p.H = d->H;
   p.G = d->H / d->cache.H_kv;
-  p.rows = dsa::kPaRows;
-  p.head_tiles = (p.G + p.rows - 1) / p.rows;
+  p.rows = plan.rows;
+  p.head_tiles = plan.head_tiles;
   p.window = d->window;
   // tokens that share a sequence read the same slots: head by head, so that one
   // head's slots stay in L2 while all its tokens pass
   p.head_major = p.T > p.g.num_seqs;
-  const int step = fp8 ? dsa::PaSmem<true>::kStep : dsa::PaSmem<false>::kStep;
-  p.gran_shift = std::min(fp8 ? 5 : 4, p.g.page_shift);            // a step at most
-  int64_t most_steps = (p.g.capacity() + step - 1) / step;
+  const int unit = std::min(plan.step, 32);
+  int unit_shift = unit == 32 ? 5 : 4;
+  int64_t most_steps = (p.g.capacity() + plan.step - 1) / plan.step;
   if (d->window > 0 || list)       // a window may begin inside a step
-    most_steps = std::min<int64_t>(most_steps, (d->window + 31) / step + 2);
+    most_steps = std::min<int64_t>(most_steps, (static_cast<int64_t>(d->window) + 31) / plan.step + 2);
+  p.gran_shift = std::min(unit_shift, p.g.page_shift);
   if (list) {
     p.block_shift = __builtin_ctz(static_cast<unsigned>(d->block_size));
     p.num_blocks = d->num_blocks;
     p.block_heads = d->block_heads;
     p.gran_shift = std::min(p.gran_shift, p.block_shift);
     p.list_steps = static_cast<int>(
-        (static_cast<int64_t>(d->num_blocks) * d->block_size + step - 1) / step);
+        (static_cast<int64_t>(d->num_blocks) * d->block_size + plan.step - 1) / plan.step);
     most_steps += p.list_steps;
   }
   p.scale_log2 = d->sm_scale * dsa::kPaLog2e;
@@ -146,8 +154,8 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
   p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kWorkspaceHeader);
-  p.part_ml = reinterpret_cast<float2 *>(p.part_o + part_floats());
-  p.chain = reinterpret_cast<int4 *>(p.part_ml + static_cast<size_t>(kPaGrid) * 2 * dsa::kPaRows);
+  p.part_ml = reinterpret_cast<float2 *>(p.part_o + part_rows(plan) * dsa::kRowD);
+  p.chain = reinterpret_cast<int4 *>(p.part_ml + part_rows(plan));
   p.err = static_cast<unsigned int *>(workspace);
   p.err_info = p.err + 1;
   p.wait_limit_ns = d->wait_limit_ns ? d->wait_limit_ns : kPaWaitLimitNs;
@@ -156,24 +164,38 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   {
     const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(p.T) * p.H};
     const cuuint64_t strides[1] = {256};
-    const cuuint32_t box[2] = {64, dsa::kPaRows};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(plan.wide ? p.G : plan.rows)};
+    const int rows = 1 << p.gran_shift;
     st = make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, q, dims, strides, box);
-    if (st == DSA_OK) st = pool_map(&tk, &d->cache, k, 1 << p.gran_shift, 1 << p.gran_shift == step);
-    if (st == DSA_OK) st = pool_map(&tv, &d->cache, v, 1 << p.gran_shift, 1 << p.gran_shift == step);
+    if (st == DSA_OK) st = pool_map(&tk, &d->cache, k, rows, rows == plan.step);
+    if (st == DSA_OK) st = pool_map(&tv, &d->cache, v, rows, rows == plan.step);
     if (st != DSA_OK) return st;
   }
-  // no more CTAs than steps for their warps
+  // no more CTAs than have enough steps
+  const int least = plan.wide ? dsa::kPwLeast : dsa::kPaLeast;
   const int64_t items = static_cast<int64_t>(p.T) * p.g.H_kv * p.head_tiles;
-  const int most = std::min(kPaGrid, dev->num_sms * kPaCtasPerSm);
-  const int64_t want = items > most * dsa::kPaWarps * 2
+  const int64_t most = std::min(plan.grid, dev->num_sms * (plan.wide ? 1 : kPaCtasPerSm));
+  const int64_t want = items > most * least
                            ? most
-                           : (items * std::max<int64_t>(1, most_steps) + 2 * dsa::kPaWarps - 1) / (2 * dsa::kPaWarps);
-  const int grid = static_cast<int>(std::min<int64_t>(most, want));
-  if (list)
-    return fp8 ? launch<true, true>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 3, stream)
-               : launch<false, true>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 2, stream);
-  return fp8 ? launch<true, false>(p, tq, tk, tv, grid, dev, kAttrPagedAttn + 1, stream)
-             : launch<false, false>(p, tq, tk, tv, grid, dev, kAttrPagedAttn, stream);
+                           : (items * std::max<int64_t>(1, most_steps) + least - 1) / least;
+  const int grid = static_cast<int>(std::min(most, want));
+  const int variant = (plan.wide ? 4 : plan.fp8 ? 1 : 0) + (list ? (plan.wide ? 1 : 2) : 0);
+  static const AttnFn fns[6] = {
+      dsa::paged_attention_kernel<false, false>, dsa::paged_attention_kernel<true, false>,
+      dsa::paged_attention_kernel<false, true>,  dsa::paged_attention_kernel<true, true>,
+      dsa::paged_attention_wide_kernel<false>,   dsa::paged_attention_wide_kernel<true>};
+  const int smem = plan.wide  ? dsa::PwSmem::kTotal
+                   : plan.fp8 ? dsa::PaSmem<true>::kTotal
+                              : dsa::PaSmem<false>::kTotal;
+  st = ensure_smem_attr(dev, kAttrPagedAttn + variant, fns[variant], smem);
+  if (st != DSA_OK) return st;
+  if (launch_pdl(fns[variant], grid, plan.wide ? dsa::kPwThreads : dsa::kPaThreads,
+                 static_cast<size_t>(smem), stream, 0, tq, tk, tv, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  if (launch_pdl(dsa::paged_attention_join_kernel, grid * (plan.rows / 2), dsa::kPaJoinThreads, 0, stream,
+                 0, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  return DSA_OK;
 }
 
 }  // namespace
@@ -188,7 +210,7 @@ dsa_status_t dsa_paged_attention_workspace_size(const dsa_paged_attention_desc_t
   if (!bytes) return DSA_ERR_INVALID_ARG;
   const dsa_status_t st = check_attn(desc, desc && desc->num_blocks != 0);
   if (st != DSA_OK) return st;
-  *bytes = workspace_bytes_needed();
+  *bytes = workspace_bytes_needed(plan_of(desc));
   return DSA_OK;
 }
 

@@ -26,6 +26,7 @@ namespace dsa {
 constexpr int kPaWarps = 4;                        // consumer warps
 constexpr int kPaThreads = (kPaWarps + 1) * 32;    // and the producer
 constexpr int kPaRows = 16;                        // query heads of a work item
+constexpr int kPaLeast = 2 * kPaWarps;             // steps worth a CTA
 
 __device__ __forceinline__ void cp_async4_zfill(void *smem_dst, const void *gmem_src,
                                                 uint32_t src_bytes) {
@@ -181,9 +182,8 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   }
   grid_dep_wait();
   grid_dep_launch_dependents();
-  // at least two steps a warp
   const PaRange range =
-      pa_range<kList, kStep, kPaThreads>(p, 2 * kPaWarps, tid, scan, start_row, start_step);
+      pa_range<kList, kStep, kPaThreads>(p, kPaLeast, tid, scan, start_row, start_step);
   if (range.begin >= range.end) {
     if (tid == 0) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;

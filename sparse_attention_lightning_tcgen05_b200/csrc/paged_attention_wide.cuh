@@ -1,0 +1,492 @@
+// paged_attention_wide.cuh -- attention over a paged bf16 cache for many query
+// heads on one key-value head (17 .. 128), for sm_100a.
+//
+// The same sums as paged_attention.cuh. With G heads on a key the products
+// cost 4 G D flops for the 4 D bytes of a key and a value, past what mma.sync
+// sustains at HBM speed from about 32 heads on; here both are tcgen05.mma with
+// all heads as the M = 128 rows, so that a slot is loaded once for all of them:
+//   S = Q K^T  (128 rows x 128 slots, K = D) from shared memory into TMEM,
+//   O += P V   (128 rows x D, K = 128 slots) with P read from TMEM, where the
+//              softmax wrote it over S, and V MN-major from the tile TMA wrote.
+// Tiles of 128 slots alternate between two streams, each with its own S (128
+// TMEM columns), O (128 columns), running maxima and sums, and softmax warps,
+// so that one stream's products run under the other's softmax; the streams
+// are added up at the item's end. Warps 0-3 and 4-7: the streams' softmax, a
+// thread a row; warp 8 issues the products; warp 9 loads.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "paged_attention.cuh"
+#include "paged_schedule.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dsa {
+
+constexpr int kPwTile = 128;                       // slots a tile
+constexpr int kPwUnit = 32;                        // slots a lookup round's unit
+constexpr int kPwRows = 128;                       // query heads of a work item, at most
+constexpr int kPwStages = 3;
+constexpr int kPwLeast = 2;                        // tiles worth a CTA
+constexpr int kPwMmaWarp = 8;
+constexpr int kPwThreads = 10 * 32;
+
+struct PwSmem {
+  static constexpr int kHalf = kPwTile * 128;                       // [128 x 128 B], half of a row each
+  static constexpr int kTileBytes = 2 * kHalf;
+  static constexpr int off_q = 0;
+  static constexpr int off_k = kTileBytes;
+  static constexpr int off_v = off_k + kPwStages * kTileBytes;
+  static constexpr int off_ml = off_v + kPwStages * kTileBytes;     // [2 streams][128 rows] (max, sum)
+  static constexpr int off_mask = off_ml + 2 * kPwRows * 8;         // [stages][4]
+  static constexpr int off_bar = off_mask + kPwStages * 16;
+  static constexpr int off_misc = off_bar + 32 * 8;
+  static constexpr int kTotal = off_misc + 192;
+  static_assert(kTotal <= 227 * 1024, "one CTA an SM");
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc]: bf16, A's row i in lane i, two
+// consecutive K elements a 32-bit column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <bool kList>
+__global__ void __launch_bounds__(kPwThreads, 1)
+    paged_attention_wide_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                                const __grid_constant__ CUtensorMap tmap_k,
+                                const __grid_constant__ CUtensorMap tmap_v, const PagedAttnParams p) {
+  using Smem = PwSmem;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint32_t *const masks = reinterpret_cast<uint32_t *>(smem + Smem::off_mask);
+  uint64_t *const k_full = reinterpret_cast<uint64_t *>(smem + Smem::off_bar);
+  uint64_t *const v_full = k_full + kPwStages;
+  uint64_t *const k_empty = v_full + kPwStages;
+  uint64_t *const v_empty = k_empty + kPwStages;
+  uint64_t *const q_full = v_empty + kPwStages;
+  uint64_t *const q_empty = q_full + 1;
+  uint64_t *const s_full = q_empty + 1;                             // [2]
+  uint64_t *const p_full = s_full + 2;                              // [2]
+  uint64_t *const pv_done = p_full + 2;                             // [2]
+  uint64_t *const item_done = pv_done + 2;
+  uint64_t *const ml_full = item_done + 1;
+  uint64_t *const o_free = ml_full + 1;
+  PaItem *const info = reinterpret_cast<PaItem *>(smem + Smem::off_misc);
+  volatile int *const abort_flag = reinterpret_cast<volatile int *>(info + 1);
+  int *const start_row = reinterpret_cast<int *>(info + 1) + 1;
+  uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(info + 1) + 2;
+  int64_t *const start_step = reinterpret_cast<int64_t *>(smem + Smem::off_misc + 32);
+  int64_t *const scan = start_step + 1;                             // [10]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == kPwMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kPwStages; ++i) {
+      mbar_init(k_full + i, kPwTile / kPwUnit);
+      mbar_init(v_full + i, kPwTile / kPwUnit);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_empty + i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 9);                         // the softmax warps and the last Q K^T
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(pv_done + i, 1);
+    }
+    mbar_init(item_done, 1);
+    mbar_init(ml_full, 8);
+    mbar_init(o_free, 8);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmap_q);
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  tc_fence_before_sync();
+  const PaRange range =
+      pa_range<kList, kPwTile, kPwThreads>(p, kPwLeast, tid, scan, start_row, start_step);
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.err, p.err_info, p.wait_limit_ns};
+
+  if (range.begin >= range.end) {
+    if (tid == 0) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  } else if (warp > kPwMmaWarp) {
+    // ---------------- producer ----------------
+    constexpr int kSub = kPwTile / kPwUnit;
+    PaCursor<kList, kPwTile> cur;
+    cur.start(p, range.outer, *start_row, *start_step, range.end - range.begin);
+    PaLookup<kList, kPwTile, kPwUnit> look;
+    look.start(p, lane, cur);
+    int4 chain = make_int4(-1, 0, 0, 0);
+    const int gran = 1 << p.gran_shift;
+    const int per_unit = look.per_unit(p);
+    const int q_rows = min(kPwRows, p.G);
+    uint32_t g = 0, n_items = 0;                              // units before this round, items
+    uint32_t my_st = 0, my_ph = 0, round = 0;
+    bool ok = true, published = false;
+    while (ok) {
+      const bool more = cur.steps > 0;
+      const bool whole = cur.steps == cur.row.steps;
+      const int kvh = cur.id(p);                              // one item a head
+      if (!pa_wait(q_empty, (n_items & 1u) ^ 1u, ctl, 70)) break;
+      if (lane == 0) {
+        *info = PaItem{more ? cur.t : -1, kvh, cur.steps, whole ? -1 : cur.first == 0 ? 1 : 0};
+        if (more) {
+          const int q_row = cur.t * p.H + kvh * p.G;
+          mbar_arrive_expect_tx(q_full, 2 * q_rows * 128);
+          tma_load_2d(smem + Smem::off_q, &tmap_q, q_full, 0, q_row);
+          tma_load_2d(smem + Smem::off_q + Smem::kHalf, &tmap_q, q_full, 64, q_row);
+        } else {
+          mbar_arrive(q_full);
+        }
+      }
+      __syncwarp();
+      if (!more) {
+        published = true;
+        break;
+      }
+      ++n_items;
+      if (!whole && cur.first == 0) {
+        const int64_t last = range.end - cur.left + cur.row.steps - 1;
+        chain = make_int4(cur.t, kvh, static_cast<int>(((last + 1) * range.ctas - 1) / range.total), 0);
+      }
+      uint32_t mask = 0, live = 0;                            // of this lane's unit
+      const int units = cur.steps * kSub;
+      for (int unit = 0; unit < units;) {
+        const int in_look = unit & (look.batch(p) - 1);
+        if (in_look == 0) {
+          look.next(p, lane);
+          live = look.hi > look.lo;
+          mask = live ? ((2u << (look.hi - 1)) - (1u << look.lo)) << look.within(p, lane) : 0u;
+          for (int off = 1; off < per_unit; off <<= 1) {
+            mask |= __shfl_xor_sync(0xffffffffu, mask, off);
+            live += __shfl_xor_sync(0xffffffffu, live, off);
+          }
+        }
+        const int count = min(min(4, look.batch(p) - in_look), units - unit);
+        const int mine = (lane / per_unit) - in_look;         // this lane's unit of the round
+        bool todo = mine >= 0 && mine < count;
+        const uint32_t my_unit = g + (todo ? mine : 0);
+        const uint32_t tile = my_unit / kSub, sub = my_unit % kSub;
+        my_st = tile % kPwStages;
+        my_ph = (tile / kPwStages) & 1u;
+        const int head = lane & ~(per_unit - 1);
+        PaPatience patience;
+        while (ok) {
+          const uint32_t free_heads = __ballot_sync(
+              0xffffffffu, todo && lane == head && mbar_test_wait(k_empty + my_st, my_ph ^ 1u) &&
+                               mbar_test_wait(v_empty + my_st, my_ph ^ 1u));
+          const bool go = todo && (free_heads >> head & 1u);
+          if (go && lane == head) {
+            masks[my_st * kSub + sub] = mask;
+            const uint32_t bytes = live * (gran * 256);
+            mbar_arrive_expect_tx(k_full + my_st, bytes);
+            mbar_arrive_expect_tx(v_full + my_st, bytes);
+          }
+          __syncwarp();
+          if (go && look.hi > look.lo) {
+            const int at = (sub * kPwUnit + look.within(p, lane)) * 128;
+            uint8_t *const kd = smem + Smem::off_k + my_st * Smem::kTileBytes + at;
+            uint8_t *const vd = smem + Smem::off_v + my_st * Smem::kTileBytes + at;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              tma_load_5d(kd + b * Smem::kHalf, &tmap_k, k_full + my_st, 0, look.slot, b, kvh, look.page);
+              tma_load_5d(vd + b * Smem::kHalf, &tmap_v, v_full + my_st, 0, look.slot, b, kvh, look.page);
+            }
+          }
+          round |= free_heads;
+          todo = todo && !go;
+          if (!__any_sync(0xffffffffu, todo)) break;
+          ok = patience.more(ctl, 71);
+        }
+        if (!ok) break;
+        round = 0;
+        g += count;
+        unit += count;
+      }
+      if (!ok) break;
+      cur.advance(p);
+    }
+    if (lane == 0) p.chain[blockIdx.x] = chain;
+    // every copy started here lands before the CTA can exit: the last tiles'
+    // barriers. (Where a wait was given up inside a tile its barrier lacks the
+    // arrivals of the units that never started; they are made here.)
+    const uint32_t started = g + __popc(round);
+    if (lane == 0) {
+      for (uint32_t u = started; u % kSub != 0; ++u) {
+        mbar_arrive(k_full + u / kSub % kPwStages);
+        mbar_arrive(v_full + u / kSub % kPwStages);
+      }
+      const uint32_t tiles = (started + kSub - 1) / kSub;
+      for (uint32_t t = tiles > kPwStages ? tiles - kPwStages : 0; t < tiles; ++t) {
+        mbar_drain(k_full + t % kPwStages, (t / kPwStages) & 1u, p.drain_limit_ns);
+        mbar_drain(v_full + t % kPwStages, (t / kPwStages) & 1u, p.drain_limit_ns);
+      }
+      if (!published && n_items > 0) mbar_drain(q_full, (n_items - 1) & 1u, p.drain_limit_ns);
+    }
+    __syncwarp();
+  } else if (warp == kPwMmaWarp) {
+    // ---------------- products ----------------
+    const uint32_t idesc_s = idesc_bf16_f32(128, kPwTile);
+    const uint32_t idesc_o = idesc_bf16_f32_bmn(128, kRowD);
+    const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem + Smem::off_q));
+    uint64_t *last_commit = nullptr;
+    uint32_t last_phase = 0;
+    uint32_t g = 0;                                           // tiles before this item
+    bool ok = true;
+    // O += P V of tile `t` (global number); fresh: its stream's first of the item
+    auto pv = [&](uint32_t t, bool fresh, uint32_t n) -> bool {
+      const uint32_t sb = t & 1u, st = t % kPwStages;
+      if (!pa_wait(p_full + sb, (t >> 1) & 1u, ctl, 72) ||
+          !pa_wait(v_full + st, (t / kPwStages) & 1u, ctl, 73) ||
+          (fresh && n > 0 && !pa_wait(o_free, (n - 1) & 1u, ctl, 74)))
+        return false;
+      tc_fence_after_sync();
+      if (lane == 0) {
+        const uint32_t v_base = smem_u32(smem + Smem::off_v + st * Smem::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kPwTile / 16; ++kk)
+          // V: 16 slots = two 8-row atoms further along K; the halves of D apart
+          mma_f16_ts(tmem + 256 + sb * 128, tmem + sb * 128 + kk * 8,
+                     sdesc_mnmajor_sw128(v_base + kk * 2048, Smem::kHalf, 1024), idesc_o,
+                     fresh && kk == 0 ? 0u : 1u);
+        mma_commit(pv_done + sb);
+        mma_commit(v_empty + st);
+        last_commit = pv_done + sb;
+        last_phase = (t >> 1) & 1u;
+      }
+      __syncwarp();
+      return true;
+    };
+    for (uint32_t n = 0; ok; ++n) {
+      if (!pa_wait(q_full, n & 1u, ctl, 75)) break;
+      const PaItem it = *info;
+      if (it.row < 0) break;
+      tc_fence_after_sync();
+      for (int i = 0; i < it.steps; ++i) {
+        const uint32_t t = g + i, sb = t & 1u, st = t % kPwStages;
+        // S's buffer is free: P V of tile t - 2, which reads P there, was
+        // issued before and products run in order
+        if (!pa_wait(k_full + st, (t / kPwStages) & 1u, ctl, 76)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(smem + Smem::off_k + st * Smem::kTileBytes));
+#pragma unroll
+          for (int kk = 0; kk < kRowD / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (Smem::kHalf >> 4) + (kk % 4) * 2;
+            mma_f16_ss(tmem + sb * 128, q_desc + off, k_desc + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(s_full + sb);
+          mma_commit(k_empty + st);
+          if (i == it.steps - 1) mma_commit(q_empty);
+          last_commit = s_full + sb;
+          last_phase = (t >> 1) & 1u;
+        }
+        __syncwarp();
+        if (i >= 1 && !pv(t - 1, i <= 2, n)) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok || !pv(g + it.steps - 1, it.steps <= 2, n)) break;
+      if (lane == 0) mma_commit(item_done);
+      __syncwarp();
+      g += it.steps;
+    }
+    if (lane == 0 && last_commit) mbar_drain(last_commit, last_phase, p.drain_limit_ns);
+    __syncwarp();
+  } else {
+    // ---------------- softmax and epilogue: a thread a row ----------------
+    const int stream = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + stream * 128, t_o = tmem + lane_base + 256 + stream * 128;
+    float2 *const ml = reinterpret_cast<float2 *>(smem + Smem::off_ml);
+    const float neg_inf = __int_as_float(0xff800000);
+    const bool mine = r < p.G;                                // rows past G hold no head
+    const bool warp_rows = (warp & 3) * 32 < p.G;
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      if (!pa_wait(q_full, n & 1u, ctl, 77)) break;
+      const PaItem it = *info;
+      if (it.row < 0) break;
+      pa_release(q_empty, lane);
+      float m = neg_inf, mb = 0.f, lazy = neg_inf, sum = 0.f;
+      bool first = true;
+      for (int i = (stream ^ g) & 1; i < it.steps; i += 2) {
+        const uint32_t t = g + i, st = t % kPwStages;
+        if (!pa_wait(s_full + stream, (t >> 1) & 1u, ctl, 78) ||
+            !pa_wait(v_full + st, (t / kPwStages) & 1u, ctl, 79)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        uint32_t mw[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mw[w] = masks[st * 4 + w];
+        const bool every = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu;
+        if (!every && !(masks[st * 4 + (r >> 5)] >> (r & 31) & 1u)) {
+          // a value row that is not kept: its weight is 0, and 0 times
+          // whatever is there has to be 0
+          uint8_t *const row = smem + Smem::off_v + st * Smem::kTileBytes + r * 128;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4 *>(row + (c >> 3) * Smem::kHalf + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (warp_rows) {
+          // P in packed pairs, from 32 logits at a time, against the running
+          // maximum as it is; where that turns out too low (the first tile, a
+          // growth past 2^8) O is rescaled and S, still in TMEM, gone over again
+          uint32_t pk[64];
+          float part = 0.f;
+          for (bool again = false;; again = true) {
+            float mx = neg_inf;
+            part = 0.f;
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              float x[32];
+              tmem_ld32_wait(t_s + 32 * q4, x);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
+              if (!every) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(mw[q4] >> c & 1u)) x[c] = neg_inf;
+              }
+              float m4[4] = {mx, neg_inf, neg_inf, neg_inf}, s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c]);
+              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float e0 = ex2_approx(x[2 * c]), e1 = ex2_approx(x[2 * c + 1]);
+                s4[c & 3] += e0 + e1;
+                pk[16 * q4 + c] = pack_bf16x2(e0, e1);
+              }
+              part += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            }
+            const bool grow = !again && mine && mx > lazy;
+            if (!__any_sync(0xffffffffu, grow)) break;
+            const float mn = grow ? mx + mb : mb;             // the row's new reference
+            const float a = !grow ? 1.f : m == neg_inf ? 0.f : ex2_approx(m - mn);
+            if (!first) {
+              // O holds the stream's earlier tiles: wait for their P V
+              if (!pa_wait(pv_done + stream, ((t >> 1) - 1) & 1u, ctl, 80)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4) {
+                float o[32];
+                tmem_ld32_wait(t_o + 32 * q4, o);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] *= a;
+                tmem_st32(t_o + 32 * q4, o);
+              }
+              tmem_wait_st();
+            }
+            sum *= a;
+            if (grow) {
+              m = mb = mn;
+              lazy = kPaLazy;
+            }
+          }
+          if (!ok) break;
+          sum += part;
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            tmem_st32(t_s + 32 * half, *reinterpret_cast<const float (*)[32]>(&pk[32 * half]));
+          tmem_wait_st();
+        }
+        first = false;
+        fence_proxy_async_smem();                             // zeroed value rows
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + stream);
+      }
+      if (!ok) break;
+      // ---- add the two streams up: this one writes half of the features ----
+      // (once everyone has read the last item's maxima and sums)
+      if (n > 0 && !pa_wait(o_free, (n - 1) & 1u, ctl, 83)) break;
+      ml[stream * kPwRows + r] = make_float2(m, sum);
+      pa_release(ml_full, lane);
+      if (!pa_wait(ml_full, n & 1u, ctl, 81) || !pa_wait(item_done, n & 1u, ctl, 82)) break;
+      tc_fence_after_sync();
+      if (warp_rows) {
+        const float2 x0 = ml[r], x1 = ml[kPwRows + r];
+        const float M = fmaxf(x0.x, x1.x);
+        const bool any0 = x0.x != neg_inf, any1 = x1.x != neg_inf;
+        const float a0 = any0 ? ex2_approx(x0.x - M) : 0.f, a1 = any1 ? ex2_approx(x1.x - M) : 0.f;
+        const float L = a0 * x0.y + a1 * x1.y;
+        const int64_t row = it.slot < 0 ? static_cast<int64_t>(it.row) * p.H + it.item * p.G + r
+                                        : (static_cast<int64_t>(blockIdx.x) * 2 + it.slot) * kPwRows + r;
+        float inv = 1.f;
+        if (it.slot < 0) {
+          float den = L;
+          if (mine && p.sinks && M != neg_inf)
+            den += ex2_approx(__ldg(p.sinks + it.item * p.G + r) * kPaLog2e - M);
+          inv = M == neg_inf ? 0.f : 1.f / den;
+          if (mine && stream == 0 && p.lse) p.lse[row] = M == neg_inf ? neg_inf : (M + log2f(L)) * kPaLn2;
+        } else if (mine && stream == 0) {
+          p.part_ml[row] = make_float2(M, L);
+        }
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+          const int c0 = 64 * stream + 32 * q2;
+          float o0[32], o1[32];
+          __syncwarp();
+          tmem_ld32_wait(tmem + lane_base + 256 + c0, o0);
+          tmem_ld32_wait(tmem + lane_base + 384 + c0, o1);
+          // a stream without a tile (or a kept slot) left no O of this item
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            o0[c] = ((any0 ? a0 * o0[c] : 0.f) + (any1 ? a1 * o1[c] : 0.f)) * inv;
+          if (!mine) {
+          } else if (it.slot < 0) {
+            uint4 *const dst = reinterpret_cast<uint4 *>(p.out + row * kRowD + c0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              dst[c] = make_uint4(pack_bf16x2(o0[8 * c], o0[8 * c + 1]), pack_bf16x2(o0[8 * c + 2], o0[8 * c + 3]),
+                                  pack_bf16x2(o0[8 * c + 4], o0[8 * c + 5]),
+                                  pack_bf16x2(o0[8 * c + 6], o0[8 * c + 7]));
+          } else {
+            float4 *const dst = reinterpret_cast<float4 *>(p.part_o + row * kRowD + c0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c] = make_float4(o0[4 * c], o0[4 * c + 1], o0[4 * c + 2], o0[4 * c + 3]);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      g += it.steps;
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kPwMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace dsa
