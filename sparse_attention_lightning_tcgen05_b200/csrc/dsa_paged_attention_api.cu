@@ -179,6 +179,8 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
                            ? most
                            : (items * std::max<int64_t>(1, most_steps) + least - 1) / least;
   const int grid = static_cast<int>(std::min(most, want));
+  p.chain_by_item = items <= grid;
+  const int entries = static_cast<int>(std::min<int64_t>(items, grid));
   const int variant = (plan.wide ? 4 : plan.fp8 ? 1 : 0) + (list ? (plan.wide ? 1 : 2) : 0);
   static const AttnFn fns[6] = {
       dsa::paged_attention_kernel<false, false>, dsa::paged_attention_kernel<true, false>,
@@ -192,8 +194,11 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   if (launch_pdl(fns[variant], grid, plan.wide ? dsa::kPwThreads : dsa::kPaThreads,
                  static_cast<size_t>(smem), stream, 0, tq, tk, tv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
-  if (launch_pdl(dsa::paged_attention_join_kernel, grid * (plan.rows / 2), dsa::kPaJoinThreads, 0, stream,
-                 0, p) != cudaSuccess)
+  const bool long_chains = 8 * items <= grid;
+  const auto join = long_chains ? dsa::paged_attention_join_kernel<8> : dsa::paged_attention_join_kernel<1>;
+  const int join_blocks =
+      entries * (plan.rows / (long_chains ? dsa::kPaJoinHeads<8> : dsa::kPaJoinHeads<1>));
+  if (launch_pdl(join, join_blocks, dsa::kPaJoinThreads, 0, stream, 0, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   return DSA_OK;
 }

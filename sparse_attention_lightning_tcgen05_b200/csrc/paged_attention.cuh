@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   const PaRange range =
       pa_range<kList, kStep, kPaThreads>(p, kPaLeast, tid, scan, start_row, start_step);
   if (range.begin >= range.end) {
-    if (tid == 0) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    PaChain{}.finish(p, tid);
     return;
   }
   const WaitCtl ctl{abort_flag, p.err, p.err_info, p.wait_limit_ns};
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     cur.start(p, range.outer, *start_row, *start_step, range.end - range.begin);
     PaLookup<kList, kStep, kStep> look;
     look.start(p, lane, cur);
-    int4 chain = make_int4(-1, 0, 0, 0);
+    PaChain chain;
     const int gran = 1 << p.gran_shift;
     const int per_step = look.per_unit(p);                    // lookups and boxes a step
     uint32_t g = 0, st = 0, ph = 0, n_items = 0;
@@ -225,11 +225,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         break;
       }
       ++n_items;
-      if (!whole && cur.first == 0) {
-        // the CTA that holds the item's last step
-        const int64_t last = range.end - cur.left + cur.row.steps - 1;
-        chain = make_int4(cur.t, id, static_cast<int>(((last + 1) * range.ctas - 1) / range.total), 0);
-      }
+      chain.add(p, range, lane, cur.t, id, range.end - cur.left, cur.first, cur.steps, cur.row.steps);
       // Rounds of up to four steps, a lane a granule: the first lane of a step
       // watches its stage, and as soon as that is free the step's lanes issue
       // their boxes. (A step at a time, with its lookup broadcast to the warp,
@@ -317,7 +313,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       if (!ok) break;
       cur.advance(p);
     }
-    if (lane == 0) p.chain[blockIdx.x] = chain;
+    chain.finish(p, lane);
     // every copy started here lands before the CTA can exit, whatever the
     // consumers' waits come to: the last round's (where it was given up), and
     // the last one of each stage before it
@@ -687,54 +683,89 @@ __global__ void __launch_bounds__(kPaThreads, 2)
 }
 
 // Joins the items that several CTAs share: an item that begins in CTA a
-// (chain.x, chain.y: its row and item) goes on through CTAs a + 1 .. chain.z.
-// Two heads a block; a lane joins one 4-feature piece of a head over the
-// partials in CTA order.
-constexpr int kPaJoinThreads = 64;
+// (chain: a row, its item there, a and the last CTA) left a partial result in
+// a's second place and in the first place of a + 1 .. last. kWays warps a head,
+// a 4-feature piece a lane, each over every kWays-th partial with kBatch of
+// them in flight, added up through shared memory in warp order. Eight ways
+// where items are few and their partials many (37 partials of 128 heads: 20 us
+// by one warp a head and one at a time, 12 us eight at a time, 3 us so); one
+// way, and fewer blocks, where most items lie in one or two CTAs (296 CTAs'
+// entries with eight ways: 10 us, with one: 3).
+constexpr int kPaJoinThreads = 512;
+template <int kWays>
+constexpr int kPaJoinHeads = kPaJoinThreads / 32 / kWays;     // of a block
+template <int kWays>
 __global__ void __launch_bounds__(kPaJoinThreads) paged_attention_join_kernel(
     const PagedAttnParams p) {
+  constexpr int kBatch = kWays > 1 ? 8 : 4;
+  __shared__ float4 acc_of[kPaJoinHeads<kWays>][kWays][32];
+  __shared__ float2 ml_of[kPaJoinHeads<kWays>][kWays];
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int pairs = p.rows / 2;
-  const int a = blockIdx.x / pairs;
-  const int r = (blockIdx.x - a * pairs) * 2 + (threadIdx.x >> 5);
-  const int4 c = p.chain[a];
+  const int blocks = p.rows / kPaJoinHeads<kWays>;
+  const int entry = blockIdx.x / blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = warp / kWays, way = warp - head * kWays;
+  const int r = (blockIdx.x - entry * blocks) * kPaJoinHeads<kWays> + head;
+  const int4 c = p.chain[entry];
   if (c.x < 0) return;
   const int kvh = c.y / p.head_tiles, ht = c.y - kvh * p.head_tiles;
-  if (r >= min(p.rows, p.G - ht * p.rows)) return;
-  const int lane = threadIdx.x & 31;
+  const bool in = r < min(p.rows, p.G - ht * p.rows);
   const float neg_inf = __int_as_float(0xff800000);
-  const int b = c.z;                                          // the last CTA of the item
-  float M = neg_inf;
-  for (int i = a + lane; i <= b; i += 32)
-    M = fmaxf(M, p.part_ml[(static_cast<int64_t>(i) * 2 + (i == a)) * p.rows + r].x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const int a = c.z, b = c.w;
+  // this warp's partials
+  float M = neg_inf, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-  for (int i0 = a; i0 <= b; i0 += 32) {
-    float w = 0.f, l = 0.f;
-    if (i0 + lane <= b) {
-      const int i = i0 + lane;
-      const float2 ml = p.part_ml[(static_cast<int64_t>(i) * 2 + (i == a)) * p.rows + r];
-      w = ml.x == neg_inf ? 0.f : ex2_approx(ml.x - M);
-      l = ml.y;
+  for (int i0 = a + way; in && i0 <= b; i0 += kBatch * kWays) {
+    float2 ml[kBatch];
+    float4 x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kWays;
+      const int64_t row = (static_cast<int64_t>(i) * 2 + (i == a)) * p.rows + r;
+      ml[j] = make_float2(neg_inf, 0.f);
+      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i <= b) {
+        ml[j] = __ldcg(p.part_ml + row);
+        x[j] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + row * kRowD) + lane);
+      }
     }
-    L += w * l;
-    const int n = min(32, b - i0 + 1);
-    for (int j = 0; j < n; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      const int i = i0 + j;
-      const float4 x = *reinterpret_cast<const float4 *>(
-          p.part_o + ((static_cast<int64_t>(i) * 2 + (i == a)) * p.rows + r) * kRowD + 4 * lane);
-      acc.x += wj * x.x;
-      acc.y += wj * x.y;
-      acc.z += wj * x.z;
-      acc.w += wj * x.w;
+    float top = M;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) top = fmaxf(top, ml[j].x);
+    if (top == neg_inf) continue;
+    const float old = M == neg_inf ? 0.f : ex2_approx(M - top);
+    M = top;
+    L *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float w = ml[j].x == neg_inf ? 0.f : ex2_approx(ml[j].x - M);
+      L = fmaf(w, ml[j].y, L);
+      acc.x = fmaf(w, x[j].x, acc.x);
+      acc.y = fmaf(w, x[j].y, acc.y);
+      acc.z = fmaf(w, x[j].z, acc.z);
+      acc.w = fmaf(w, x[j].w, acc.w);
     }
   }
+  acc_of[head][way][lane] = acc;
+  if (lane == 0) ml_of[head][way] = make_float2(M, L);
+  __syncthreads();
+  if (way != 0 || !in) return;
+  for (int w = 0; w < kWays; ++w) M = fmaxf(M, ml_of[head][w].x);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  L = 0.f;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  for (int w = 0; w < kWays; ++w) {
+    const float2 ml = ml_of[head][w];
+    const float4 x = acc_of[head][w][lane];
+    const float f = ml.x == neg_inf ? 0.f : ex2_approx(ml.x - M);
+    L = fmaf(f, ml.y, L);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
   const int h = kvh * p.G + ht * p.rows + r;
   const int64_t orow = static_cast<int64_t>(c.x) * p.H + h;
   float den = L;

@@ -59,6 +59,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
       : "memory");
 }
 
+// Eight floats, a whole 32-byte sector, in one store (dst 32-byte aligned).
+__device__ __forceinline__ void st_global_v8(float *dst, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 template <bool kList>
 __global__ void __launch_bounds__(kPwThreads, 1)
     paged_attention_wide_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -124,7 +131,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   const WaitCtl ctl{abort_flag, p.err, p.err_info, p.wait_limit_ns};
 
   if (range.begin >= range.end) {
-    if (tid == 0) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    PaChain{}.finish(p, tid);
   } else if (warp > kPwMmaWarp) {
     // ---------------- producer ----------------
     constexpr int kSub = kPwTile / kPwUnit;
@@ -132,7 +139,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     cur.start(p, range.outer, *start_row, *start_step, range.end - range.begin);
     PaLookup<kList, kPwTile, kPwUnit> look;
     look.start(p, lane, cur);
-    int4 chain = make_int4(-1, 0, 0, 0);
+    PaChain chain;
     const int gran = 1 << p.gran_shift;
     const int per_unit = look.per_unit(p);
     const int q_rows = min(kPwRows, p.G);
@@ -161,10 +168,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         break;
       }
       ++n_items;
-      if (!whole && cur.first == 0) {
-        const int64_t last = range.end - cur.left + cur.row.steps - 1;
-        chain = make_int4(cur.t, kvh, static_cast<int>(((last + 1) * range.ctas - 1) / range.total), 0);
-      }
+      chain.add(p, range, lane, cur.t, kvh, range.end - cur.left, cur.first, cur.steps, cur.row.steps);
       uint32_t mask = 0, live = 0;                            // of this lane's unit
       const int units = cur.steps * kSub;
       for (int unit = 0; unit < units;) {
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (!ok) break;
       cur.advance(p);
     }
-    if (lane == 0) p.chain[blockIdx.x] = chain;
+    chain.finish(p, lane);
     // every copy started here lands before the CTA can exit: the last tiles'
     // barriers. (Where a wait was given up inside a tile its barrier lacks the
     // arrivals of the units that never started; they are made here.)
@@ -352,55 +356,45 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             *reinterpret_cast<uint4 *>(row + (c >> 3) * Smem::kHalf + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
         }
         if (warp_rows) {
-          // P in packed pairs, from 32 logits at a time, against the running
-          // maximum as it is; where that turns out too low (the first tile, a
-          // growth past 2^8) O is rescaled and S, still in TMEM, gone over again
-          uint32_t pk[64];
-          float part = 0.f;
-          for (bool again = false;; again = true) {
-            float mx = neg_inf;
-            part = 0.f;
+          // S is read twice, 32 logits at a time: for the maximum, and once O is
+          // on the right reference for P, which takes S's place as packed
+          // pairs (columns already read)
+          float v[2][32];
+          const bool down_scale = p.scale_log2 < 0.f;
+          float m4[4] = {neg_inf, neg_inf, neg_inf, neg_inf};
+          tmem_ld32_async(t_s, v[0]);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              float x[32];
-              tmem_ld32_wait(t_s + 32 * q4, x);
+          for (int q4 = 0; q4 < 4; ++q4) {
+            float (&x)[32] = v[q4 & 1];
+            tmem_wait_ld32(x);
+            if (q4 < 3) tmem_ld32_async(t_s + 32 * (q4 + 1), v[(q4 + 1) & 1]);
+            if (!every || down_scale) {
+              // masked logits out; a negative scale turns the order around
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
-              if (!every) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(mw[q4] >> c & 1u)) x[c] = neg_inf;
-              }
-              float m4[4] = {mx, neg_inf, neg_inf, neg_inf}, s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c]);
-              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float e0 = ex2_approx(x[2 * c]), e1 = ex2_approx(x[2 * c + 1]);
-                s4[c & 3] += e0 + e1;
-                pk[16 * q4 + c] = pack_bf16x2(e0, e1);
-              }
-              part += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+              for (int c = 0; c < 32; ++c)
+                x[c] = mw[q4] >> c & 1u ? (down_scale ? -x[c] : x[c]) : neg_inf;
             }
-            const bool grow = !again && mine && mx > lazy;
-            if (!__any_sync(0xffffffffu, grow)) break;
-            const float mn = grow ? mx + mb : mb;             // the row's new reference
+#pragma unroll
+            for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c]);
+          }
+          tmem_ld32_async(t_s, v[0]);                         // for the second reading
+          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          // a logit of the row's largest, or -inf where nothing is kept
+          const float mx = top == neg_inf ? neg_inf : top * fabsf(p.scale_log2);
+          const bool grow = mine && mx - mb > lazy;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mx : mb;                  // the row's new reference
             const float a = !grow ? 1.f : m == neg_inf ? 0.f : ex2_approx(m - mn);
             if (!first) {
-              // O holds the stream's earlier tiles: wait for their P V
-              if (!pa_wait(pv_done + stream, ((t >> 1) - 1) & 1u, ctl, 80)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
+              // O holds the stream's earlier tiles: their P V ended before this
+              // tile's S, which products issued in order
+              tmem_wait_ld32(v[0]);
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4) {
-                float o[32];
-                tmem_ld32_wait(t_o + 32 * q4, o);
+                tmem_ld32_wait(t_o + 32 * q4, v[1]);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] *= a;
-                tmem_st32(t_o + 32 * q4, o);
+                for (int c = 0; c < 32; ++c) v[1][c] *= a;
+                tmem_st32(t_o + 32 * q4, v[1]);
               }
               tmem_wait_st();
             }
@@ -410,11 +404,34 @@ __global__ void __launch_bounds__(kPwThreads, 1)
               lazy = kPaLazy;
             }
           }
-          if (!ok) break;
-          sum += part;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            tmem_st32(t_s + 32 * half, *reinterpret_cast<const float (*)[32]>(&pk[32 * half]));
+          for (int half = 0; half < 2; ++half) {
+            float pk[32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int q4 = 2 * half + q;
+              float (&x)[32] = v[q4 & 1];
+              tmem_wait_ld32(x);
+              if (q4 < 3) tmem_ld32_async(t_s + 32 * (q4 + 1), v[(q4 + 1) & 1]);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
+              if (!every) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(mw[q4] >> c & 1u)) x[c] = neg_inf;
+              }
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float e0 = ex2_approx(x[2 * c]), e1 = ex2_approx(x[2 * c + 1]);
+                s4[c & 3] += e0 + e1;
+                pk[16 * q + c] = __uint_as_float(pack_bf16x2(e0, e1));
+              }
+            }
+            // columns 32 half .. + 31: their logits have been read twice
+            tmem_st32(t_s + 32 * half, pk);
+          }
+          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
           tmem_wait_st();
         }
         first = false;
@@ -469,10 +486,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                                   pack_bf16x2(o0[8 * c + 4], o0[8 * c + 5]),
                                   pack_bf16x2(o0[8 * c + 6], o0[8 * c + 7]));
           } else {
-            float4 *const dst = reinterpret_cast<float4 *>(p.part_o + row * kRowD + c0);
+            float *const dst = p.part_o + row * kRowD + c0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(o0[4 * c], o0[4 * c + 1], o0[4 * c + 2], o0[4 * c + 3]);
+            for (int c = 0; c < 4; ++c) st_global_v8(dst + 8 * c, &o0[8 * c]);
           }
         }
       }

@@ -38,7 +38,8 @@ struct PagedAttnParams {
   float *lse;
   float *part_o;               // [grid, 2, rows, D] unnormalised
   float2 *part_ml;             // [grid, 2, rows] (max in log2 units, sum)
-  int4 *chain;                 // [grid] items that several CTAs share
+  int4 *chain;                 // items that several CTAs share (PaChain)
+  bool chain_by_item;          // an entry an item, else one a CTA
   unsigned int *err, *err_info;
   uint64_t wait_limit_ns, drain_limit_ns;
 };
@@ -48,6 +49,40 @@ struct PagedAttnParams {
 __device__ __forceinline__ int pa_inner(const PagedAttnParams &p) {
   return p.head_major ? p.head_tiles : p.g.H_kv * p.head_tiles;
 }
+
+// A CTA's range of all items' steps, [begin, end) of `total`, one of `ctas` that
+// have any; and the group of items it starts in.
+struct PaRange {
+  int64_t begin, end, total, ctas;
+  int outer;
+};
+
+// The entries that tell the join kernel which items several CTAs share, written
+// by the CTA in which an item begins: (row, item of the row, first and last
+// CTA), row -1 for an item that lies in one CTA. By item where there are no
+// more of them than CTAs, else by CTA: one, since only its last item can go on.
+struct PaChain {
+  int4 mine = {-1, 0, 0, 0};
+
+  // an item of which this CTA has `steps` of `of` steps from `first` on, the
+  // first of them number `at` of all
+  __device__ __forceinline__ void add(const PagedAttnParams &p, const PaRange &range, int lane, int row,
+                                      int id, int64_t at, int first, int steps, int of) {
+    if (first != 0) return;
+    int4 e = {-1, 0, 0, 0};
+    if (steps < of)
+      e = make_int4(row, id, static_cast<int>(blockIdx.x),
+                    static_cast<int>(((at + of) * range.ctas - 1) / range.total));
+    if (p.chain_by_item) {
+      if (lane == 0) p.chain[static_cast<int64_t>(row) * p.g.H_kv * p.head_tiles + id] = e;
+    } else {
+      mine = e;
+    }
+  }
+  __device__ __forceinline__ void finish(const PagedAttnParams &p, int lane) const {
+    if (!p.chain_by_item && lane == 0) p.chain[blockIdx.x] = mine;
+  }
+};
 
 // What a query token attends to: its sequence, last slot and recent slots.
 struct PaRow {
@@ -216,13 +251,8 @@ struct PaLookup {
   }
 };
 
-// A CTA's range of all items' steps, the group and row it starts in and the
-// offset there; called by all kThreads threads. `least`: steps below which
-// a CTA is not worth its part of the join.
-struct PaRange {
-  int64_t begin, end, total, ctas;
-  int outer;
-};
+// Called by all kThreads threads. `least`: steps below which a CTA is not worth
+// its part of the join.
 template <bool kList, int kStep, int kThreads>
 __device__ __forceinline__ PaRange pa_range(const PagedAttnParams &p, int least, int tid, int64_t *scan,
                                             int *start_row, int64_t *start_step) {
