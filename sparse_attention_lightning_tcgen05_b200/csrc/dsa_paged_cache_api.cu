@@ -62,6 +62,20 @@ AppendFn append_fn(bool halves) {
   return halves ? dsa::cache_append_kernel<kQ, kKv, true> : dsa::cache_append_kernel<kQ, kKv, false>;
 }
 
+using PoolFn = void (*)(const dsa::PoolParams);
+
+template <bool kFp8>
+PoolFn pool_fn(bool pow2, int block_size) {
+  if (!pow2) return dsa::block_pool_kernel<kFp8, 0>;
+  switch (block_size) {
+    case 1: return dsa::block_pool_kernel<kFp8, 1>;
+    case 2: return dsa::block_pool_kernel<kFp8, 2>;
+    case 4: return dsa::block_pool_kernel<kFp8, 4>;
+    case 8: return dsa::block_pool_kernel<kFp8, 8>;
+    default: return dsa::block_pool_kernel<kFp8, 16>;
+  }
+}
+
 dsa_status_t check_append(const dsa_append_desc_t *d) {
   if (!d) return DSA_ERR_INVALID_ARG;
   dsa_status_t st = check_paged_cache(&d->cache);
@@ -199,16 +213,19 @@ dsa_status_t dsa_block_pool(const dsa_block_pool_desc_t *desc, const void *k_cac
   dsa::PoolParams p{};
   p.g = paged_geom(&c);
   p.block_size = desc->block_size;
-  // 16 slots a half warp: the run it looks up at once
+  // a run of 16 slots a half warp
+  const bool pow2 = (p.block_size & (p.block_size - 1)) == 0;
   p.share = 1;
-  while (p.share < dsa::kPoolGroups && p.share * 16 < p.block_size) p.share *= 2;
-  p.together = std::max(1, 16 / p.block_size);
+  while (p.share < dsa::kPoolGroups && p.share * dsa::kPoolRun < p.block_size) p.share *= 2;
+  p.together = pow2 ? std::max(1, dsa::kPoolRun / p.block_size) : 1;
   const int per_cta = dsa::kPoolGroups / p.share;
   const int64_t sets = (p.g.capacity() / p.block_size + p.together - 1) / p.together;
   // the kernel numbers up to kPoolSeqs sequences' items in 32 bits
   if (sets * c.H_kv > INT32_MAX / std::min(c.num_seqs, dsa::kPoolSeqs)) return DSA_ERR_UNSUPPORTED;
+  const bool fp8 = c.dtype != DSA_KV_BF16;
   const int64_t most = (sets * c.H_kv * c.num_seqs + per_cta - 1) / per_cta;
-  const int blocks = static_cast<int>(std::min<int64_t>(most, dev->num_sms * 3));   // one wave
+  const int wave = dev->num_sms * (fp8 ? dsa::kPoolCtasPerSm<true> : dsa::kPoolCtasPerSm<false>);
+  const int blocks = static_cast<int>(std::min<int64_t>(most, wave));
   p.S_pool = desc->S_pool;
   p.seq_stride = desc->seq_stride;
   p.head_stride = desc->head_stride;
@@ -219,7 +236,7 @@ dsa_status_t dsa_block_pool(const dsa_block_pool_desc_t *desc, const void *k_cac
   p.pooled = pooled;
   p.pooled_scale = pooled_scale;
   p.last_block = last_block;
-  const auto fn = c.dtype == DSA_KV_BF16 ? dsa::block_pool_kernel<false> : dsa::block_pool_kernel<true>;
+  const PoolFn fn = fp8 ? pool_fn<true>(pow2, p.block_size) : pool_fn<false>(pow2, p.block_size);
   if (launch_pdl(fn, blocks, dsa::kPoolThreads, 0,
                  reinterpret_cast<cudaStream_t>(stream), 0, p) != cudaSuccess)
     return DSA_ERR_CUDA;

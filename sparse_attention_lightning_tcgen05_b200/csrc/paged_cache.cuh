@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 struct PoolParams {
   PagedGeom g;
   int block_size;
-  int share;                 // half warps a pooled row (1 .. kPoolGroups, a power of two)
-  int together;              // pooled rows a half warp sums at once (1 where share > 1)
+  int share;                 // half warps that sum one pooled row (1 .. kPoolGroups, a power of two)
+  int together;              // blocks of an item: 16 slots' (1 where share > 1)
   int64_t S_pool, seq_stride, head_stride;
   const void *k;
   const uint8_t *k_scale;
@@ -300,12 +300,15 @@ struct PoolParams {
 constexpr int kPoolThreads = 256;
 constexpr int kPoolLanes = 16;           // lanes a key row, 8 features each
 constexpr int kPoolGroups = kPoolThreads / kPoolLanes;
-constexpr int kPoolBatch = 8;            // key rows a half warp has in flight
+constexpr int kPoolRun = 16;             // key rows a half warp has in flight
+constexpr int kPoolSeqs = 1024;          // sequences the CTAs share out at once
+template <bool kFp8>
+constexpr int kPoolCtasPerSm = kFp8 ? 3 : 2;   // a run is 64 or 32 registers
 
 // One pooled row, 8 features a lane; called by whole warps.
 template <bool kFp8>
-__device__ __forceinline__ void pool_store(const float (&x)[8], const PoolParams &p, int seq,
-                                           int h, int b, int l, bool write) {
+__device__ __forceinline__ void pool_store(const float (&x)[8], const PoolParams &p, int seq, int h,
+                                           int b, int l, bool write) {
   const int64_t at = seq * p.seq_stride + h * p.head_stride + static_cast<int64_t>(b) * kRowD;
   if constexpr (kFp8) {
     uint32_t top = largest_bits(x);
@@ -326,9 +329,7 @@ __device__ __forceinline__ void pool_store(const float (&x)[8], const PoolParams
   }
 }
 
-constexpr int kPoolSeqs = 1024;          // sequences the CTAs share out at once
-
-// First fresh block of a sequence, and one past the last.
+// First fresh block of a sequence, and one past the last to write.
 __device__ __forceinline__ int2 pool_range(const PoolParams &p, int seq, int &done) {
   const int cap = static_cast<int>(p.g.capacity());
   const int pos = __ldg(p.positions + seq);
@@ -338,15 +339,57 @@ __device__ __forceinline__ int2 pool_range(const PoolParams &p, int seq, int &do
   return make_int2(first, static_cast<int>(min(static_cast<int64_t>(done), p.S_pool)));
 }
 
-// All sequences' fresh blocks (runs of `together` blocks of a head: the items)
-// are counted by every CTA, which then takes an equal share of them, so that
-// sequences of any lengths fill the GPU evenly. A half warp looks 16 slots up
-// at once (a lane each) and reads their rows in batches of eight: the slots of
-// `together` small blocks, or a run of a large block that `share` half warps
-// sum; the first of those joins the sums (in order, so that the result does
-// not depend on timing) and writes the row.
+// A lane's 8 features of a key row, as loaded.
 template <bool kFp8>
-__global__ void __launch_bounds__(kPoolThreads) block_pool_kernel(const PoolParams p) {
+struct PoolRaw {
+  uint4 w;
+};
+template <>
+struct PoolRaw<true> {
+  uint2 w;
+};
+
+template <bool kFp8>
+__device__ __forceinline__ PoolRaw<kFp8> pool_load(const PoolParams &p, int64_t at, int l) {
+  PoolRaw<kFp8> r;
+  if constexpr (kFp8)
+    r.w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.k) + at) + l);
+  else
+    r.w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + at) + l);
+  return r;
+}
+
+// acc += the row's features (fp8: under the scale byte e)
+template <bool kFp8>
+__device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &r, uint32_t e) {
+  if constexpr (kFp8) {
+    const float f = e8m0_f32(e);
+    const uint32_t q[4] = {r.w.x & 0xffffu, r.w.x >> 16, r.w.y & 0xffffu, r.w.y >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = ffma2(e4m3x2_f32(q[i]), make_float2(f, f), acc[i]);
+  } else {
+    float v[8];
+    unpack8(r.w, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i].x += v[2 * i];
+      acc[i].y += v[2 * i + 1];
+    }
+  }
+}
+
+// All sequences' fresh blocks (`together` blocks of a head: an item) are
+// counted by every CTA, which then takes an equal share of them, so that
+// sequences of any lengths fill the GPU evenly. kR > 0: block sizes that are
+// powers of two, kR = min(block_size, 16). A half warp reads the 16 rows of a
+// run (one page's, 16 slots from a multiple of 16 on) at once, looking the next
+// item's run up meanwhile: 16 / kR blocks, or 1/16 of a larger block's rows and
+// on, which `share` half warps sum and the first of them joins (in order, so
+// that the result does not depend on timing). kR = 0: any block size, each row
+// looked up by itself.
+template <bool kFp8, int kR>
+__global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
+    block_pool_kernel(const PoolParams p) {
   __shared__ float part[kPoolGroups][kRowD];
   __shared__ uint32_t ends[kPoolSeqs];                      // items up to and with a sequence's
   __shared__ uint32_t warp_sum[kPoolThreads / 32];
@@ -368,7 +411,9 @@ __global__ void __launch_bounds__(kPoolThreads) block_pool_kernel(const PoolPara
       count[i] = 0;
       if (s < seqs) {
         const int2 r = pool_range(p, seq0 + s, done);
-        if (r.y > r.x) count[i] = static_cast<uint32_t>((r.y - r.x + p.together - 1) / p.together) * p.g.H_kv;
+        // items lie at multiples of `together` blocks
+        if (r.y > r.x)
+          count[i] = static_cast<uint32_t>((r.y + p.together - 1) / p.together - r.x / p.together) * p.g.H_kv;
         if (p.last_block && blockIdx.x == 0)
           for (int h = 0; h < p.g.H_kv; ++h)
             p.last_block[static_cast<int64_t>(seq0 + s) * p.g.H_kv + h] = done - 1;
@@ -381,7 +426,7 @@ __global__ void __launch_bounds__(kPoolThreads) block_pool_kernel(const PoolPara
       const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
       if ((threadIdx.x & 31) >= off) incl += o;
     }
-    __syncthreads();                                          // the last turn's readers are done
+    __syncthreads();                                        // the last turn's readers are done
     if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = incl;
     __syncthreads();
     uint32_t items = 0, at0 = incl - sum;
@@ -394,116 +439,129 @@ __global__ void __launch_bounds__(kPoolThreads) block_pool_kernel(const PoolPara
     for (int i = 0; i < kEach; ++i) ends[threadIdx.x * kEach + i] = at0 += count[i];
     __syncthreads();
     // ---- this CTA's share, in turns of per_cta items ----
-    const uint32_t turns_all = (items + per_cta - 1) / per_cta;
-    const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(turns_all) * blockIdx.x / gridDim.x) * per_cta;
-    const uint32_t end = min(items, static_cast<uint32_t>(static_cast<uint64_t>(turns_all) * (blockIdx.x + 1) /
-                                                         gridDim.x) * per_cta);
-    int s = 0;
-    {
-      // the sequence of this half warp's first item
-      int hi = seqs - 1;
-      while (s < hi) {
-        const int mid = (s + hi) / 2;
-        if (begin + mine < ends[mid]) hi = mid;
-        else s = mid + 1;
-      }
+    const uint64_t turns_all = (items + per_cta - 1) / per_cta;
+    const uint32_t begin = static_cast<uint32_t>(turns_all * blockIdx.x / gridDim.x) * per_cta;
+    const uint32_t end =
+        min(items, static_cast<uint32_t>(turns_all * (blockIdx.x + 1) / gridDim.x) * per_cta);
+    int s = 0;                                              // the sequence of this half warp's item
+    for (int hi = seqs - 1; s < hi;) {
+      const int mid = (s + hi) / 2;
+      if (begin + mine < ends[mid]) hi = mid;
+      else s = mid + 1;
     }
-    for (uint32_t it0 = begin; it0 < end; it0 += per_cta) {
-      const uint32_t it = it0 + mine;
-      const bool in = it < end;
-      while (in && it >= ends[s]) ++s;
-      const int seq = seq0 + s;
+    // Where an item is: its sequence and head, its first block and those to
+    // write ([lo, hi)), and element offset and page of this half warp's first run.
+    struct Item {
+      int seq, h, b0, lo, hi;
+      int64_t at;
+    };
+    auto locate = [&](uint32_t it) -> Item {
+      Item x{0, 0, 0, 0, 0, -1};
+      if (it >= end) return x;
+      while (it >= ends[s]) ++s;
+      x.seq = seq0 + s;
       int done;
-      const int2 range = pool_range(p, seq, done);
-      const uint32_t local = in ? it - (s > 0 ? ends[s - 1] : 0) : 0;
+      const int2 range = pool_range(p, x.seq, done);
+      const uint32_t local = it - (s > 0 ? ends[s - 1] : 0);
       const uint32_t set = local / static_cast<uint32_t>(p.g.H_kv);
-      const int h = static_cast<int>(local - set * p.g.H_kv);
-      const int b0 = range.x + static_cast<int>(set) * p.together;
-      const int blocks = in ? min(p.together, range.y - b0) : 0;
-      const int slot0 = b0 * p.block_size;
-      const int slots = blocks * p.block_size;                       // of this half warp's set
-      const int64_t head_off = h * p.g.head_stride;
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      int left = p.block_size, b = b0;                               // slots until the block ends
-      // a run of 16 slots a time; every lane of the warp takes as many turns
-      const int turns = (p.together * p.block_size + 16 * p.share - 1) / (16 * p.share);
-      for (int turn = 0; turn < turns; ++turn) {
-        const int j0 = (turn * p.share + part_of) * 16;
-        int64_t at = -1;
-        uint32_t sc = 0x7f7f7f7fu;
-        if (j0 + l < slots) at = paged_slot(p.g, seq, slot0 + j0 + l);
-        if (at >= 0) at += head_off;
-        if (kFp8 && at >= 0) sc = __ldg(reinterpret_cast<const uint32_t *>(p.k_scale + at / 32));
+      x.h = static_cast<int>(local - set * p.g.H_kv);
+      x.b0 = (range.x / p.together + static_cast<int>(set)) * p.together;
+      x.lo = max(x.b0, range.x);
+      x.hi = min(x.b0 + p.together, range.y);
+      if constexpr (kR > 0) x.at = paged_slot(p.g, x.seq, x.b0 * p.block_size + part_of * kPoolRun);
+      return x;
+    };
+    Item next = locate(begin + mine);
+    for (uint32_t it0 = begin; it0 < end; it0 += per_cta) {
+      const Item cur = next;
+      float2 acc[4];
 #pragma unroll
-        for (int j1 = 0; j1 < 16; j1 += kPoolBatch) {
-          if (j1 >= p.together * p.block_size) break;                // the same for all lanes
-          uint4 w[kPoolBatch];
-          uint32_t f[kPoolBatch];
+      for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
+      if constexpr (kR > 0) {
+        const bool in = cur.hi > cur.lo;
+        for (int j0 = part_of * kPoolRun;;) {
+          const int64_t at = j0 == part_of * kPoolRun
+                                 ? cur.at
+                                 : paged_slot(p.g, cur.seq, cur.b0 * p.block_size + j0);
+          const int64_t base = at + cur.h * p.g.head_stride;
+          PoolRaw<kFp8> w[kPoolRun];
+          uint32_t sc = 0x7f7f7f7fu;                        // scales of the run's row l
 #pragma unroll
-          for (int u = 0; u < kPoolBatch; ++u) {
-            const int64_t a = __shfl_sync(0xffffffffu, at, j1 + u, kPoolLanes);
-            w[u] = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (kFp8) {
-              f[u] = __shfl_sync(0xffffffffu, sc, j1 + u, kPoolLanes) >> (8 * (l >> 2)) & 0xffu;
-              if (a >= 0) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.k) + a) + l);
-                w[u].x = v.x;
-                w[u].y = v.y;
-              }
-            } else {
-              if (a >= 0)
-                w[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) + a) + l);
-            }
+          for (int u = 0; u < kPoolRun; ++u) {
+            w[u].w = {};
+            if (at >= 0) w[u] = pool_load<kFp8>(p, base + u * p.g.slot_stride, l);
           }
+          if (kFp8 && at >= 0)
+            sc = __ldg(reinterpret_cast<const uint32_t *>(p.k_scale + (base + l * p.g.slot_stride) / 32));
+          if (j0 == part_of * kPoolRun) next = locate(it0 + per_cta + mine);
+          j0 += kPoolRun * p.share;
+          const bool on = kR == 16 && j0 < p.block_size;    // the same for all lanes
 #pragma unroll
-          for (int u = 0; u < kPoolBatch; ++u) {
-            if constexpr (kFp8) {
-              const float e = e8m0_f32(f[u]);
-              const uint32_t q[4] = {w[u].x & 0xffffu, w[u].x >> 16, w[u].y & 0xffffu, w[u].y >> 16};
+          for (int u = 0; u < kPoolRun; ++u) {
+            uint32_t e = 0;
+            if constexpr (kFp8) e = __shfl_sync(0xffffffffu, sc, u, kPoolLanes) >> (8 * (l >> 2)) & 0xffu;
+            pool_add<kFp8>(acc, w[u], e);
+            if (kR < 16 && u % (kR > 0 ? kR : 1) == kR - 1) {
+              // a block ends; its size is a power of two: the product is the quotient
+              const int b = cur.b0 + u / (kR > 0 ? kR : 1);
+              float x[8];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float2 v = e4m3x2_f32(q[i]);
-                acc[2 * i] = fmaf(v.x, e, acc[2 * i]);
-                acc[2 * i + 1] = fmaf(v.y, e, acc[2 * i + 1]);
+                x[2 * i] = acc[i].x * (1.f / (kR > 0 ? kR : 1));
+                x[2 * i + 1] = acc[i].y * (1.f / (kR > 0 ? kR : 1));
+                acc[i] = make_float2(0.f, 0.f);
               }
-            } else {
-              float v[8];
-              unpack8(w[u], v);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) acc[i] += v[i];
-            }
-            if (p.share == 1) {
-              // a block ends: write its mean and start over
-              const bool end = --left == 0;
-              if (__any_sync(0xffffffffu, end)) {
-                if (end) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) acc[i] = __fdiv_rn(acc[i], size);
-                }
-                pool_store<kFp8>(acc, p, seq, h, b, l, end && b - b0 < blocks);
-                if (end) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-                  left = p.block_size;
-                  ++b;
-                }
-              }
+              pool_store<kFp8>(x, p, cur.seq, cur.h, b, l, in && b >= cur.lo && b < cur.hi);
             }
           }
+          if (!on) break;
         }
+      } else {
+        // rows part_of, part_of + share, ..: four in flight
+        const bool in = cur.hi > cur.lo;
+        for (int j0 = part_of; j0 < p.block_size; j0 += 4 * p.share) {
+          PoolRaw<kFp8> w[4];
+          uint32_t e[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int j = j0 + u * p.share;
+            int64_t at = -1;
+            if (in && j < p.block_size) at = paged_slot(p.g, cur.seq, cur.b0 * p.block_size + j);
+            w[u].w = {};
+            e[u] = 127;
+            if (at >= 0) {
+              at += cur.h * p.g.head_stride;
+              w[u] = pool_load<kFp8>(p, at, l);
+              if (kFp8) e[u] = __ldg(p.k_scale + at / 32 + (l >> 2));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) pool_add<kFp8>(acc, w[u], e[u]);
+        }
+        next = locate(it0 + per_cta + mine);
       }
-      if (p.share > 1) {
+      if (kR == 16 || kR == 0) {
+        if (p.share > 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[grp][8 * l + i] = acc[i];
-        __syncthreads();
-        if (part_of == 0)
-          for (int u = 1; u < p.share; ++u)
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(&part[grp][8 * l + 2 * i]) = acc[i];
+          __syncthreads();
+          if (part_of == 0)
+            for (int u = 1; u < p.share; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += part[grp + u][8 * l + i];
-        __syncthreads();
+              for (int i = 0; i < 4; ++i) {
+                const float2 o = *reinterpret_cast<const float2 *>(&part[grp + u][8 * l + 2 * i]);
+                acc[i].x += o.x;
+                acc[i].y += o.y;
+              }
+          __syncthreads();
+        }
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = __fdiv_rn(acc[i], size);
-        pool_store<kFp8>(acc, p, seq, h, b0, l, in && part_of == 0);
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __fdiv_rn(acc[i].x, size);
+          x[2 * i + 1] = __fdiv_rn(acc[i].y, size);
+        }
+        pool_store<kFp8>(x, p, cur.seq, cur.h, cur.b0, l, cur.hi > cur.lo && part_of == 0);
       }
     }
   }
