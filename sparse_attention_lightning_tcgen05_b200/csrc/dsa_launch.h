@@ -26,7 +26,7 @@ enum : uint32_t {
   kAttrTopkCausal = 19,
   kAttrSparseMqa = 20,
   kAttrPrepare = 21,
-  kAttrPagedAttn = 22,   // and the next five: its instances
+  kAttrPagedAttn = 22,   // and the next seven: its instances
 };
 
 // What the library knows about a device (probed once per device).

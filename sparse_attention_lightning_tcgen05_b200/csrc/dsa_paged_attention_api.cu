@@ -47,8 +47,14 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
   return DSA_OK;
 }
 
-// The kernel of a call. Wide: more than 16 heads a key-value head of a bf16
-// cache, which would otherwise read every slot more than once.
+// The kernel of a call. Wide: all query heads of a key-value head as the rows of
+// one tcgen05 tile, from more than 16 of them on (the other kernel takes 16 at a
+// time, each time with all the slots), for an fp8 cache from more than 48 on:
+// there the wide kernel's conversion bounds it whatever the heads. Four contexts
+// of 65,536 slots, one key head, us, other kernel / wide:
+//   heads        16         32         64        128
+//   bf16     32 / 34    36 / 35    59 / 37   108 / 39
+//   fp8      29 / 64    45 / 64    76 / 66   140 / 70
 struct Plan {
   bool fp8, wide;
   int rows, head_tiles, step, grid;      // grid: CTAs at most
@@ -58,7 +64,7 @@ Plan plan_of(const dsa_paged_attention_desc_t *d) {
   Plan p{};
   const int G = d->H / d->cache.H_kv;
   p.fp8 = d->cache.dtype != DSA_KV_BF16;
-  p.wide = !p.fp8 && G > dsa::kPaRows;
+  p.wide = G > (p.fp8 ? 3 : 1) * dsa::kPaRows;
   p.rows = p.wide ? dsa::kPwRows : dsa::kPaRows;
   p.head_tiles = (G + p.rows - 1) / p.rows;
   p.step = p.wide ? dsa::kPwTile : p.fp8 ? dsa::PaSmem<true>::kStep : dsa::PaSmem<false>::kStep;
@@ -181,18 +187,20 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   const int grid = static_cast<int>(std::min(most, want));
   p.chain_by_item = items <= grid;
   const int entries = static_cast<int>(std::min<int64_t>(items, grid));
-  const int variant = (plan.wide ? 4 : plan.fp8 ? 1 : 0) + (list ? (plan.wide ? 1 : 2) : 0);
-  static const AttnFn fns[6] = {
-      dsa::paged_attention_kernel<false, false>, dsa::paged_attention_kernel<true, false>,
-      dsa::paged_attention_kernel<false, true>,  dsa::paged_attention_kernel<true, true>,
-      dsa::paged_attention_wide_kernel<false>,   dsa::paged_attention_wide_kernel<true>};
-  const int smem = plan.wide  ? dsa::PwSmem::kTotal
-                   : plan.fp8 ? dsa::PaSmem<true>::kTotal
-                              : dsa::PaSmem<false>::kTotal;
+  const int variant = (plan.wide ? 4 : 0) + (plan.fp8 ? 2 : 0) + (list ? 1 : 0);
+  static const AttnFn fns[8] = {
+      dsa::paged_attention_kernel<false, false>,      dsa::paged_attention_kernel<false, true>,
+      dsa::paged_attention_kernel<true, false>,       dsa::paged_attention_kernel<true, true>,
+      dsa::paged_attention_wide_kernel<false, false>, dsa::paged_attention_wide_kernel<false, true>,
+      dsa::paged_attention_wide_kernel<true, false>,  dsa::paged_attention_wide_kernel<true, true>};
+  static const int smems[4] = {dsa::PaSmem<false>::kTotal, dsa::PaSmem<true>::kTotal,
+                               dsa::PwSmem<false>::kTotal, dsa::PwSmem<true>::kTotal};
+  static const int threads_of[4] = {dsa::kPaThreads, dsa::kPaThreads, dsa::PwSmem<false>::kThreads,
+                                    dsa::PwSmem<true>::kThreads};
+  const int smem = smems[variant >> 1], threads = threads_of[variant >> 1];
   st = ensure_smem_attr(dev, kAttrPagedAttn + variant, fns[variant], smem);
   if (st != DSA_OK) return st;
-  if (launch_pdl(fns[variant], grid, plan.wide ? dsa::kPwThreads : dsa::kPaThreads,
-                 static_cast<size_t>(smem), stream, 0, tq, tk, tv, p) != cudaSuccess)
+  if (launch_pdl(fns[variant], grid, threads, static_cast<size_t>(smem), stream, 0, tq, tk, tv, p) != cudaSuccess)
     return DSA_ERR_CUDA;
   const bool long_chains = 8 * items <= grid;
   const auto join = long_chains ? dsa::paged_attention_join_kernel<8> : dsa::paged_attention_join_kernel<1>;

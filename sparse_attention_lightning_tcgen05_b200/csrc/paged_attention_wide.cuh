@@ -1,18 +1,24 @@
-// paged_attention_wide.cuh -- attention over a paged bf16 cache for many query
-// heads on one key-value head (17 .. 128), for sm_100a.
+// paged_attention_wide.cuh -- attention over a paged cache on tcgen05, for
+// sm_100a: more than 16 query heads on a key-value head, and every fp8 cache.
 //
-// The same sums as paged_attention.cuh. With G heads on a key the products
-// cost 4 G D flops for the 4 D bytes of a key and a value, past what mma.sync
-// sustains at HBM speed from about 32 heads on; here both are tcgen05.mma with
-// all heads as the M = 128 rows, so that a slot is loaded once for all of them:
+// The same sums as paged_attention.cuh, all of a key-value head's query heads
+// (up to 128) being the M = 128 rows of both products, so that a slot is loaded
+// once for all of them:
 //   S = Q K^T  (128 rows x 128 slots, K = D) from shared memory into TMEM,
 //   O += P V   (128 rows x D, K = 128 slots) with P read from TMEM, where the
-//              softmax wrote it over S, and V MN-major from the tile TMA wrote.
+//              softmax wrote it over S, and V MN-major from its tile.
 // Tiles of 128 slots alternate between two streams, each with its own S (128
 // TMEM columns), O (128 columns), running maxima and sums, and softmax warps,
 // so that one stream's products run under the other's softmax; the streams
 // are added up at the item's end. Warps 0-3 and 4-7: the streams' softmax, a
-// thread a row; warp 8 issues the products; warp 9 loads.
+// thread a row; warp 8 issues the products; warp 9 loads. With G heads on a
+// key the products cost 4 G D flops for the 4 D bytes of a bf16 key and value,
+// past what mma.sync sustains at HBM speed from about 32 heads on.
+//
+// An fp8 cache is loaded as it is and turned into bf16 tiles by warps 10 and 11
+// (e4m3 times a power of two is exact in bf16); the rest is as for bf16. That
+// conversion, 5 instructions for two features, bounds the kernel there, whatever
+// the number of heads. (Four such warps leave the others too few registers.)
 #pragma once
 
 #include <cstdint>
@@ -28,21 +34,35 @@ namespace dsa {
 constexpr int kPwTile = 128;                       // slots a tile
 constexpr int kPwUnit = 32;                        // slots a lookup round's unit
 constexpr int kPwRows = 128;                       // query heads of a work item, at most
-constexpr int kPwStages = 3;
 constexpr int kPwLeast = 2;                        // tiles worth a CTA
 constexpr int kPwMmaWarp = 8;
-constexpr int kPwThreads = 10 * 32;
+constexpr int kPwConvertWarp = 10;                 // fp8: and the next
+constexpr int kPwConvertWarps = 2;
 
+// Shared memory: bf16 tiles as two halves of their rows ([128 x 128 bytes]
+// each, 128-byte swizzle), loaded directly or (fp8) converted from slots of a
+// staging ring, in which a tile's keys and values take a slot each.
+template <bool kFp8>
 struct PwSmem {
-  static constexpr int kHalf = kPwTile * 128;                       // [128 x 128 B], half of a row each
+  static constexpr int kThreads = (kPwConvertWarp + (kFp8 ? kPwConvertWarps : 0)) * 32;
+  // fp8: K's tile is free again while V's is being converted
+  static constexpr int kKStages = kFp8 ? 1 : 3, kVStages = kFp8 ? 2 : 3;
+  static constexpr int kSlots = kFp8 ? 5 : 0;
+  static constexpr int kHalf = kPwTile * 128;                       // [128 x 128 B]
   static constexpr int kTileBytes = 2 * kHalf;
   static constexpr int off_q = 0;
   static constexpr int off_k = kTileBytes;
-  static constexpr int off_v = off_k + kPwStages * kTileBytes;
-  static constexpr int off_ml = off_v + kPwStages * kTileBytes;     // [2 streams][128 rows] (max, sum)
-  static constexpr int off_mask = off_ml + 2 * kPwRows * 8;         // [stages][4]
-  static constexpr int off_bar = off_mask + kPwStages * 16;
-  static constexpr int off_misc = off_bar + 32 * 8;
+  static constexpr int off_v = off_k + kKStages * kTileBytes;
+  static constexpr int off_slot = off_v + kVStages * kTileBytes;
+  static constexpr int kSlotBytes = kHalf;                          // [128 x 128 B] e4m3
+  static constexpr int off_scale = off_slot + kSlots * kSlotBytes;  // [slots][128] words
+  static constexpr int off_ml = off_scale + kSlots * kPwTile * 4;   // [2 streams][128 rows] (max, sum)
+  // kept slots of a tile, in a ring that outlasts every stage between the
+  // producer and the softmax
+  static constexpr int kMasks = 8;
+  static constexpr int off_mask = off_ml + 2 * kPwRows * 8;         // [kMasks][4]
+  static constexpr int off_bar = off_mask + kMasks * 16;
+  static constexpr int off_misc = off_bar + 40 * 8;
   static constexpr int kTotal = off_misc + 192;
   static_assert(kTotal <= 227 * 1024, "one CTA an SM");
 };
@@ -66,19 +86,76 @@ __device__ __forceinline__ void st_global_v8(float *dst, const float *v) {
                : "memory");
 }
 
-template <bool kList>
-__global__ void __launch_bounds__(kPwThreads, 1)
+// 16 e4m3 features of a row as 16 bf16 values times a power of two: f1 is
+// 2^(s - 127 + 120) (bf16_of_even: a byte's bits read as bf16 are its value
+// times 2^-120), or 2^120 with f2 the scale where that is past bf16's exponents.
+__device__ __forceinline__ void bf16_of_e4m3x16(uint4 w, uint32_t f1, uint32_t f2, bool two,
+                                                uint4 (&out)[2]) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = __byte_perm(in[i >> 1], 0, i & 1 ? 0x3424 : 0x1404);   // byte, 0, next, 0
+    r[i] = mul_bf16x2((u & 0x80008000u) | (u >> 4 & 0x07f007f0u), f1);
+    if (two) r[i] = mul_bf16x2(r[i], f2);
+  }
+  out[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// A slot's staged row (with its scale word) as a row of a bf16 tile.
+__device__ __forceinline__ void convert_row(const uint8_t *slot, uint32_t scales, uint8_t *tile, int r) {
+  uint32_t nan = 0;
+  // two multiplications where a scale is 2^8 or more (or NaN): rare
+  const bool two = ((scales & 0x7f7f7f7fu) + 0x79797979u & scales & 0x80808080u) != 0;
+  uint4 in[8];                                                // (read before any store)
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    in[c] = *reinterpret_cast<const uint4 *>(slot + r * 128 + ((c ^ (r & 7)) << 4));
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 w = in[c];
+    // the code 0x7f, either sign, is a NaN
+    nan |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+           ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+    const uint32_t s = scales >> (8 * (c >> 1)) & 0xffu;
+    uint32_t f1 = (s + 120u) << 7, f2 = 0;
+    if (two) {
+      f1 = 0x7b80u;                                          // 2^120
+      f2 = s == 255u ? 0x7fc0u : s == 0u ? 0x0040u : s << 7;
+      f2 |= f2 << 16;
+    }
+    uint4 out[2];
+    bf16_of_e4m3x16(w, f1 | f1 << 16, f2, two, out);
+    uint8_t *const row = tile + (c >> 2) * (kPwTile * 128) + r * 128;
+    *reinterpret_cast<uint4 *>(row + ((((2 * c) & 7) ^ (r & 7)) << 4)) = out[0];
+    *reinterpret_cast<uint4 *>(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = out[1];
+  }
+  if (nan & 0x80808080u) {
+    for (int e = 0; e < kRowD; ++e)
+      if ((slot[r * 128 + (((e >> 4) ^ (r & 7)) << 4) + (e & 15)] & 0x7f) == 0x7f)
+        *reinterpret_cast<uint16_t *>(tile + (e >> 6) * (kPwTile * 128) + r * 128 +
+                                      ((((e >> 3) & 7) ^ (r & 7)) << 4) + 2 * (e & 7)) = 0x7fc0u;
+  }
+}
+
+template <bool kFp8, bool kList>
+__global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
     paged_attention_wide_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                 const __grid_constant__ CUtensorMap tmap_k,
                                 const __grid_constant__ CUtensorMap tmap_v, const PagedAttnParams p) {
-  using Smem = PwSmem;
+  using Smem = PwSmem<kFp8>;
+  constexpr int kKStages = Smem::kKStages, kVStages = Smem::kVStages;
+  constexpr int kSub = kPwTile / kPwUnit;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t *const masks = reinterpret_cast<uint32_t *>(smem + Smem::off_mask);
   uint64_t *const k_full = reinterpret_cast<uint64_t *>(smem + Smem::off_bar);
-  uint64_t *const v_full = k_full + kPwStages;
-  uint64_t *const k_empty = v_full + kPwStages;
-  uint64_t *const v_empty = k_empty + kPwStages;
-  uint64_t *const q_full = v_empty + kPwStages;
+  uint64_t *const v_full = k_full + kKStages;
+  uint64_t *const k_empty = v_full + kVStages;
+  uint64_t *const v_empty = k_empty + kKStages;
+  uint64_t *const slot_full = v_empty + kVStages;
+  uint64_t *const slot_empty = slot_full + Smem::kSlots;
+  uint64_t *const q_full = slot_empty + Smem::kSlots;
   uint64_t *const q_empty = q_full + 1;
   uint64_t *const s_full = q_empty + 1;                             // [2]
   uint64_t *const p_full = s_full + 2;                              // [2]
@@ -99,11 +176,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kPwStages; ++i) {
-      mbar_init(k_full + i, kPwTile / kPwUnit);
-      mbar_init(v_full + i, kPwTile / kPwUnit);
+    // tiles are filled by four units' loads, or by the converting warps
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(k_full + i, kFp8 ? kPwConvertWarps : kSub);
       mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(v_full + i, kFp8 ? kPwConvertWarps : kSub);
       mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < Smem::kSlots; ++i) {
+      mbar_init(slot_full + i, kSub * 33);        // a unit's loads and its 32 scale words
+      mbar_init(slot_empty + i, kPwConvertWarps);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 9);                         // the softmax warps and the last Q K^T
@@ -125,16 +209,43 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   grid_dep_launch_dependents();
   tc_fence_before_sync();
   const PaRange range =
-      pa_range<kList, kPwTile, kPwThreads>(p, kPwLeast, tid, scan, start_row, start_step);
+      pa_range<kList, kPwTile, Smem::kThreads>(p, kPwLeast, tid, scan, start_row, start_step);
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.err, p.err_info, p.wait_limit_ns};
 
   if (range.begin >= range.end) {
     PaChain{}.finish(p, tid);
+  } else if (kFp8 && warp >= kPwConvertWarp) {
+    // ---------------- conversion: a slot's row a thread at a time ----------------
+    const int r0 = tid - kPwConvertWarp * 32;
+    const uint32_t tiles = static_cast<uint32_t>(range.end - range.begin);
+    for (uint32_t c = 0; c < 2 * tiles; ++c) {
+      const uint32_t t = c >> 1, is_v = c & 1u;
+      const uint32_t slot = c % (Smem::kSlots + !kFp8), lap = c / (Smem::kSlots + !kFp8);
+      const uint32_t st = is_v ? t % kVStages : t % kKStages, use = is_v ? t / kVStages : t / kKStages;
+      if (!pa_wait(slot_full + slot, lap & 1u, ctl, 84) ||
+          !pa_wait((is_v ? v_empty : k_empty) + st, (use & 1u) ^ 1u, ctl, 85))
+        break;
+      const uint8_t *const from = smem + Smem::off_slot + slot * Smem::kSlotBytes;
+      uint8_t *const to = smem + (is_v ? Smem::off_v : Smem::off_k) + st * Smem::kTileBytes;
+      const uint32_t *const scales = reinterpret_cast<const uint32_t *>(smem + Smem::off_scale) + slot * kPwTile;
+      for (int r = r0; r < kPwTile; r += kPwConvertWarps * 32) {
+        if (masks[t % Smem::kMasks * kSub + (r >> 5)] >> (r & 31) & 1u) {
+          convert_row(from, scales[r], to, r);
+        } else {
+          // a slot that is not kept: whatever was staged, its row is zero
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint4 *>(to + (i >> 3) * Smem::kHalf + r * 128 + ((i & 7) << 4)) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      pa_release((is_v ? v_full : k_full) + st, lane);        // read by the products (async proxy)
+      if (lane == 0) mbar_arrive(slot_empty + slot);
+    }
   } else if (warp > kPwMmaWarp) {
     // ---------------- producer ----------------
-    constexpr int kSub = kPwTile / kPwUnit;
     PaCursor<kList, kPwTile> cur;
     cur.start(p, range.outer, *start_row, *start_step, range.end - range.begin);
     PaLookup<kList, kPwTile, kPwUnit> look;
@@ -144,7 +255,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const int per_unit = look.per_unit(p);
     const int q_rows = min(kPwRows, p.G);
     uint32_t g = 0, n_items = 0;                              // units before this round, items
-    uint32_t my_st = 0, my_ph = 0, round = 0;
+    uint32_t round = 0;                                       // heads of the round that went
     bool ok = true, published = false;
     while (ok) {
       const bool more = cur.steps > 0;
@@ -187,30 +298,71 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         bool todo = mine >= 0 && mine < count;
         const uint32_t my_unit = g + (todo ? mine : 0);
         const uint32_t tile = my_unit / kSub, sub = my_unit % kSub;
-        my_st = tile % kPwStages;
-        my_ph = (tile / kPwStages) & 1u;
+        // where the unit's keys and values go: tiles, or two staging slots
+        uint64_t *kf, *vf, *ke, *ve;
+        uint8_t *kd, *vd;
+        uint32_t kp, vp;
+        if constexpr (kFp8) {
+          const uint32_t c = 2 * tile, ks = c % Smem::kSlots, vs = (c + 1) % Smem::kSlots;
+          kf = slot_full + ks;
+          vf = slot_full + vs;
+          ke = slot_empty + ks;
+          ve = slot_empty + vs;
+          kp = (c / Smem::kSlots) & 1u;
+          vp = ((c + 1) / Smem::kSlots) & 1u;
+          kd = smem + Smem::off_slot + ks * Smem::kSlotBytes;
+          vd = smem + Smem::off_slot + vs * Smem::kSlotBytes;
+        } else {
+          const uint32_t st = tile % kKStages;
+          kf = k_full + st;
+          vf = v_full + st;
+          ke = k_empty + st;
+          ve = v_empty + st;
+          kp = vp = (tile / kKStages) & 1u;
+          kd = smem + Smem::off_k + st * Smem::kTileBytes;
+          vd = smem + Smem::off_v + st * Smem::kTileBytes;
+        }
         const int head = lane & ~(per_unit - 1);
         PaPatience patience;
         while (ok) {
-          const uint32_t free_heads = __ballot_sync(
-              0xffffffffu, todo && lane == head && mbar_test_wait(k_empty + my_st, my_ph ^ 1u) &&
-                               mbar_test_wait(v_empty + my_st, my_ph ^ 1u));
+          const uint32_t free_heads =
+              __ballot_sync(0xffffffffu, todo && lane == head && mbar_test_wait(ke, kp ^ 1u) &&
+                                             mbar_test_wait(ve, vp ^ 1u));
           const bool go = todo && (free_heads >> head & 1u);
           if (go && lane == head) {
-            masks[my_st * kSub + sub] = mask;
-            const uint32_t bytes = live * (gran * 256);
-            mbar_arrive_expect_tx(k_full + my_st, bytes);
-            mbar_arrive_expect_tx(v_full + my_st, bytes);
+            masks[tile % Smem::kMasks * kSub + sub] = mask;
+            const uint32_t bytes = live * (gran * (kFp8 ? 128 : 256));
+            mbar_arrive_expect_tx(kf, bytes);
+            mbar_arrive_expect_tx(vf, bytes);
           }
           __syncwarp();
           if (go && look.hi > look.lo) {
             const int at = (sub * kPwUnit + look.within(p, lane)) * 128;
-            uint8_t *const kd = smem + Smem::off_k + my_st * Smem::kTileBytes + at;
-            uint8_t *const vd = smem + Smem::off_v + my_st * Smem::kTileBytes + at;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              tma_load_5d(kd + b * Smem::kHalf, &tmap_k, k_full + my_st, 0, look.slot, b, kvh, look.page);
-              tma_load_5d(vd + b * Smem::kHalf, &tmap_v, v_full + my_st, 0, look.slot, b, kvh, look.page);
+            for (int b = 0; b < (kFp8 ? 1 : 2); ++b) {
+              tma_load_5d(kd + b * Smem::kHalf + at, &tmap_k, kf, 0, look.slot, b, kvh, look.page);
+              tma_load_5d(vd + b * Smem::kHalf + at, &tmap_v, vf, 0, look.slot, b, kvh, look.page);
+            }
+          }
+          if constexpr (kFp8) {
+            // the scales of the units that just went, a lane a slot
+            for (uint32_t left = free_heads; left != 0; left &= left - 1) {
+              const int h = __ffs(left) - 1;
+              const uint32_t unit_no = __shfl_sync(0xffffffffu, my_unit, h);
+              const bool keep = __shfl_sync(0xffffffffu, mask, h) >> lane & 1u;
+              const int pg = __shfl_sync(0xffffffffu, look.page, h + (lane >> p.gran_shift));
+              const int sl = __shfl_sync(0xffffffffu, look.slot, h + (lane >> p.gran_shift));
+              const int64_t o = keep ? (pg * p.g.page_stride +
+                                        static_cast<int64_t>(sl + (lane & (gran - 1))) * p.g.slot_stride +
+                                        kvh * p.g.head_stride) / 32
+                                     : 0;
+              const uint32_t c = 2 * (unit_no / kSub), row = unit_no % kSub * kPwUnit + lane;
+              uint32_t *const sc = reinterpret_cast<uint32_t *>(smem + Smem::off_scale);
+              const uint32_t ks = c % Smem::kSlots, vs = (c + 1) % Smem::kSlots;
+              cp_async4_zfill(sc + ks * kPwTile + row, p.k_scale + o, keep ? 4u : 0u);
+              cp_async_mbar_arrive_noinc(slot_full + ks);
+              cp_async4_zfill(sc + vs * kPwTile + row, p.v_scale + o, keep ? 4u : 0u);
+              cp_async_mbar_arrive_noinc(slot_full + vs);
             }
           }
           round |= free_heads;
@@ -228,18 +380,30 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     }
     chain.finish(p, lane);
     // every copy started here lands before the CTA can exit: the last tiles'
-    // barriers. (Where a wait was given up inside a tile its barrier lacks the
+    // barriers. (Where a wait was given up inside a tile its barriers lack the
     // arrivals of the units that never started; they are made here.)
+    if constexpr (kFp8) cp_async_wait<0>();
+    __syncwarp();
     const uint32_t started = g + __popc(round);
     if (lane == 0) {
-      for (uint32_t u = started; u % kSub != 0; ++u) {
-        mbar_arrive(k_full + u / kSub % kPwStages);
-        mbar_arrive(v_full + u / kSub % kPwStages);
-      }
-      const uint32_t tiles = (started + kSub - 1) / kSub;
-      for (uint32_t t = tiles > kPwStages ? tiles - kPwStages : 0; t < tiles; ++t) {
-        mbar_drain(k_full + t % kPwStages, (t / kPwStages) & 1u, p.drain_limit_ns);
-        mbar_drain(v_full + t % kPwStages, (t / kPwStages) & 1u, p.drain_limit_ns);
+      auto barrier = [&](uint32_t c, uint32_t &phase) -> uint64_t * {
+        if constexpr (kFp8) {
+          phase = (c / Smem::kSlots) & 1u;
+          return slot_full + c % Smem::kSlots;
+        } else {
+          phase = (c / 2 / kKStages) & 1u;
+          return (c & 1u ? v_full : k_full) + c / 2 % kKStages;
+        }
+      };
+      const uint32_t loads = 2 * ((started + kSub - 1) / kSub);          // keys and values of a tile
+      uint32_t phase;
+      for (uint32_t u = started; u % kSub != 0; ++u)
+        for (uint32_t c = loads - 2; c < loads; ++c)
+          for (int i = 0; i < (kFp8 ? 33 : 1); ++i) mbar_arrive(barrier(c, phase));
+      constexpr uint32_t kLast = kFp8 ? Smem::kSlots : 2 * kKStages;
+      for (uint32_t c = loads > kLast ? loads - kLast : 0; c < loads; ++c) {
+        uint64_t *const bar = barrier(c, phase);
+        mbar_drain(bar, phase, p.drain_limit_ns);
       }
       if (!published && n_items > 0) mbar_drain(q_full, (n_items - 1) & 1u, p.drain_limit_ns);
     }
@@ -255,9 +419,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     bool ok = true;
     // O += P V of tile `t` (global number); fresh: its stream's first of the item
     auto pv = [&](uint32_t t, bool fresh, uint32_t n) -> bool {
-      const uint32_t sb = t & 1u, st = t % kPwStages;
+      const uint32_t sb = t & 1u, st = t % kVStages;
       if (!pa_wait(p_full + sb, (t >> 1) & 1u, ctl, 72) ||
-          !pa_wait(v_full + st, (t / kPwStages) & 1u, ctl, 73) ||
+          !pa_wait(v_full + st, (t / kVStages) & 1u, ctl, 73) ||
           (fresh && n > 0 && !pa_wait(o_free, (n - 1) & 1u, ctl, 74)))
         return false;
       tc_fence_after_sync();
@@ -283,10 +447,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (it.row < 0) break;
       tc_fence_after_sync();
       for (int i = 0; i < it.steps; ++i) {
-        const uint32_t t = g + i, sb = t & 1u, st = t % kPwStages;
+        const uint32_t t = g + i, sb = t & 1u, st = t % kKStages;
         // S's buffer is free: P V of tile t - 2, which reads P there, was
         // issued before and products run in order
-        if (!pa_wait(k_full + st, (t / kPwStages) & 1u, ctl, 76)) {
+        if (!pa_wait(k_full + st, (t / kKStages) & 1u, ctl, 76)) {
           ok = false;
           break;
         }
@@ -336,18 +500,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       float m = neg_inf, mb = 0.f, lazy = neg_inf, sum = 0.f;
       bool first = true;
       for (int i = (stream ^ g) & 1; i < it.steps; i += 2) {
-        const uint32_t t = g + i, st = t % kPwStages;
+        const uint32_t t = g + i, st = t % kVStages, mt = t % Smem::kMasks * kSub;
         if (!pa_wait(s_full + stream, (t >> 1) & 1u, ctl, 78) ||
-            !pa_wait(v_full + st, (t / kPwStages) & 1u, ctl, 79)) {
+            !pa_wait(v_full + st, (t / kVStages) & 1u, ctl, 79)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
         uint32_t mw[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mw[w] = masks[st * 4 + w];
+        for (int w = 0; w < 4; ++w) mw[w] = masks[mt + w];
         const bool every = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu;
-        if (!every && !(masks[st * 4 + (r >> 5)] >> (r & 31) & 1u)) {
+        if (!kFp8 && !every && !(masks[mt + (r >> 5)] >> (r & 31) & 1u)) {
           // a value row that is not kept: its weight is 0, and 0 times
           // whatever is there has to be 0
           uint8_t *const row = smem + Smem::off_v + st * Smem::kTileBytes + r * 128;
@@ -359,15 +523,17 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           // S is read twice, 32 logits at a time: for the maximum, and once O is
           // on the right reference for P, which takes S's place as packed
           // pairs (columns already read)
+          // (the next 32 on their way meanwhile)
           float v[2][32];
+          auto ahead = [&](int q4) { tmem_ld32_async(t_s + 32 * q4, v[q4 & 1]); };
           const bool down_scale = p.scale_log2 < 0.f;
           float m4[4] = {neg_inf, neg_inf, neg_inf, neg_inf};
-          tmem_ld32_async(t_s, v[0]);
+          ahead(0);
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             float (&x)[32] = v[q4 & 1];
             tmem_wait_ld32(x);
-            if (q4 < 3) tmem_ld32_async(t_s + 32 * (q4 + 1), v[(q4 + 1) & 1]);
+            if (q4 < 3) ahead(q4 + 1);
             if (!every || down_scale) {
               // masked logits out; a negative scale turns the order around
 #pragma unroll
@@ -377,7 +543,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c]);
           }
-          tmem_ld32_async(t_s, v[0]);                         // for the second reading
+          ahead(0);                                           // for the second reading
           const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           // a logit of the row's largest, or -inf where nothing is kept
           const float mx = top == neg_inf ? neg_inf : top * fabsf(p.scale_log2);
@@ -389,12 +555,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
               // O holds the stream's earlier tiles: their P V ended before this
               // tile's S, which products issued in order
               tmem_wait_ld32(v[0]);
+              float (&o)[32] = v[1];
 #pragma unroll
               for (int q4 = 0; q4 < 4; ++q4) {
-                tmem_ld32_wait(t_o + 32 * q4, v[1]);
+                tmem_ld32_wait(t_o + 32 * q4, o);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[1][c] *= a;
-                tmem_st32(t_o + 32 * q4, v[1]);
+                for (int c = 0; c < 32; ++c) o[c] *= a;
+                tmem_st32(t_o + 32 * q4, o);
               }
               tmem_wait_st();
             }
@@ -413,7 +580,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
               const int q4 = 2 * half + q;
               float (&x)[32] = v[q4 & 1];
               tmem_wait_ld32(x);
-              if (q4 < 3) tmem_ld32_async(t_s + 32 * (q4 + 1), v[(q4 + 1) & 1]);
+              if (q4 < 3) ahead(q4 + 1);
 #pragma unroll
               for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
               if (!every) {
