@@ -104,7 +104,7 @@ typedef struct {
  *                                                          (16-byte aligned)
  *  cos, sin   [T, rope_dim/2] fp32 (may be NULL when rope_dim = 0)
  *  positions  [T] int32; a negative position marks a padded token, of which
- *             nothing is read or written
+ *             nothing is written
  *  seq_ids    [T] int32, or NULL: token t belongs to sequence t
  *  q_out      [T, H, D] bf16, or e4m3 with q_scale [T, H, D/32] e8m0
  *                                                          (16-byte aligned)

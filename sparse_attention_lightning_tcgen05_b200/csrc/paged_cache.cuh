@@ -93,6 +93,43 @@ __device__ __forceinline__ uint32_t e8m0_of(uint32_t top) {
   return top < 0x7f800000u ? max(0, static_cast<int>((top + 0x1fffffu) >> 23) - 8) : 255;
 }
 
+// The largest magnitude's bits, a NaN's where there is one: one instruction a
+// feature (its result's sign, the product of the signs, is dropped).
+template <int kN>
+__device__ __forceinline__ uint32_t largest_bits(const float (&x)[kN]) {
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < kN; ++i)
+    asm("max.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(top) : "f"(x[i]));
+  return __float_as_uint(top) & 0x7fffffffu;
+}
+
+// Two products, each rounded to fp32.
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %5};\n\t"
+      "mul.rn.f32x2 pd, pa, pb;\n\t"
+      "mov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Two sums, each rounded to fp32.
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %5};\n\t"
+      "add.rn.f32x2 pd, pa, pb;\n\t"
+      "mov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // kN features (a multiple of 4) over 2^(e - 127) as e4m3 bytes; zeros for 255.
 template <int kN>
 __device__ __forceinline__ void quantize(const float (&x)[kN], uint32_t e, uint32_t (&out)[kN / 4]) {
@@ -100,18 +137,10 @@ __device__ __forceinline__ void quantize(const float (&x)[kN], uint32_t e, uint3
   const float inv = __uint_as_float(e == 255 ? 0u : (254 - e) << 23);
 #pragma unroll
   for (int i = 0; i < kN / 4; ++i) {
-    const uint32_t w = e4m3x2(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv)) |
-                       e4m3x2(__fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv)) << 16;
-    out[i] = e == 255 ? 0u : w;
+    const float2 a = fmul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(inv, inv));
+    const float2 b = fmul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(inv, inv));
+    out[i] = e == 255 ? 0u : __byte_perm(e4m3x2(a.x, a.y), e4m3x2(b.x, b.y), 0x5410);
   }
-}
-
-template <int kN>
-__device__ __forceinline__ uint32_t largest_bits(const float (&x)[kN]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kN; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  return top;
 }
 
 // ---- append --------------------------------------------------------------------
@@ -131,7 +160,7 @@ struct AppendParams {
 };
 
 constexpr int kAppendRows = 4;           // head rows a group of lanes holds at once
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 // Lanes of a head row: 16 of 8 features (a row's lines are read and written by
 // consecutive lanes) where rows stay bf16; eight of 16 where some become
@@ -164,7 +193,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
     const int r = r0 + i;
 #pragma unroll
     for (int u = 0; u < kP; ++u) raw[i][u] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && r < p.rows) {
+    if (in && r < p.rows) {                          // (a padded token's too: no wait for its position)
       const uint16_t *src = r < kv0  ? p.q + t * p.q_stride + r * kRowD
                             : r < v0 ? p.k + t * p.k_stride + (r - kv0) * kRowD
                                      : p.v + t * p.v_stride + (r - v0) * kRowD;
@@ -190,7 +219,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
       c[u][i] = 1.f;
       s[u][i] = 0.f;
     }
-    if (f < 2 * p.half && live && r0 < v0) {
+    if (f < 2 * p.half && in && r0 < v0) {
       const float *cr = p.cos + static_cast<int64_t>(t) * p.half + c0;
       const float *sr = p.sin + static_cast<int64_t>(t) * p.half + c0;
       if (p.vec) {
@@ -246,9 +275,12 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 #pragma unroll
       for (int j = 0; j < kF / 2; ++j)
         if (kF / 2 * l + j < p.half) {
-          const float a = x[2 * j], b = x[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(a, c[j >> 2][j & 3]), __fmul_rn(b, s[j >> 2][j & 3]));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(a, s[j >> 2][j & 3]), __fmul_rn(b, c[j >> 2][j & 3]));
+          // (a cos, a sin) + (-b sin, b cos)
+          const float a = x[2 * j], b = x[2 * j + 1], cj = c[j >> 2][j & 3], sj = s[j >> 2][j & 3];
+          const float2 y = fadd2(fmul2(make_float2(a, a), make_float2(cj, sj)),
+                                 fmul2(make_float2(b, b), make_float2(-sj, cj)));
+          x[2 * j] = y.x;
+          x[2 * j + 1] = y.y;
         }
     }
     // where the row goes (the fp8 rows' shuffles below are the whole warp's)
