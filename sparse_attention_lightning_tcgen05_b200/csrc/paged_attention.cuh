@@ -473,12 +473,17 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     // logit may pass it before O is rescaled (four lanes share a row's)
     float m[2] = {neg_inf, neg_inf}, mb[2] = {0.f, 0.f}, lazy[2] = {neg_inf, neg_inf};
     float sum[2] = {0.f, 0.f};
-    float s[kJ][4], s_next[kJ][4];
+    constexpr bool kAhead = !kFp8;                            // fp8: no registers for it
+    float s[kJ][4], s_next[kAhead ? kJ : 1][4];
     uint32_t mask = 0, mask_next = 0;
     const int step0 = (warp - base_g) & (kPaWarps - 1);
-    if (step0 < it.steps && !logits(base_g + step0, s, mask)) return;
+    if (kAhead && step0 < it.steps && !logits(base_g + step0, s, mask)) return;
     for (int step = step0; step < it.steps; step += kPaWarps) {
-      if (step + kPaWarps < it.steps && !logits(base_g + step + kPaWarps, s_next, mask_next)) return;
+      if constexpr (kAhead) {
+        if (step + kPaWarps < it.steps && !logits(base_g + step + kPaWarps, s_next, mask_next)) return;
+      } else {
+        if (!logits(base_g + step, s, mask)) return;
+      }
       const uint32_t st = (base_g + step) % Smem::kStages;
       uint8_t *const stage = smem + st * Smem::kStageBytes;
       const uint32_t vs = smem_u32(stage) + Smem::off_v;
@@ -564,15 +569,17 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         for (int jj = 0; jj < kJ / 2; ++jj) {
           const uint2 w0 = *reinterpret_cast<const uint2 *>(sc + 16 * jj + 2 * quad);
           const uint2 w1 = *reinterpret_cast<const uint2 *>(sc + 16 * jj + 8 + 2 * quad);
+          const float(&sa)[4] = s[2 * jj], (&sb)[4] = s[2 * jj + 1];
+          const uint32_t pr[4] = {pack_bf16x2(sa[0], sa[1]), pack_bf16x2(sa[2], sa[3]),
+                                  pack_bf16x2(sb[0], sb[1]), pack_bf16x2(sb[2], sb[3])};
 #pragma unroll
           for (int blk = 0; blk < 4; ++blk) {
-            const float f0 = __uint_as_float((w0.x >> (8 * blk) & 0xffu) << 23);
-            const float f1 = __uint_as_float((w0.y >> (8 * blk) & 0xffu) << 23);
-            const float f2 = __uint_as_float((w1.x >> (8 * blk) & 0xffu) << 23);
-            const float f3 = __uint_as_float((w1.y >> (8 * blk) & 0xffu) << 23);
-            const float(&sa)[4] = s[2 * jj], (&sb)[4] = s[2 * jj + 1];
-            const uint32_t pf[4] = {pack_bf16x2(sa[0] * f0, sa[1] * f1), pack_bf16x2(sa[2] * f0, sa[3] * f1),
-                                    pack_bf16x2(sb[0] * f2, sb[1] * f3), pack_bf16x2(sb[2] * f2, sb[3] * f3)};
+            // two slots' scale bytes as two bf16 powers of two (255: infinity,
+            // which makes a NaN of the zero data beside it)
+            const uint32_t f0 = __byte_perm(w0.x, w0.y, 0x4400 + 0x1111 * blk) << 7 & 0x7f807f80u;
+            const uint32_t f1 = __byte_perm(w1.x, w1.y, 0x4400 + 0x1111 * blk) << 7 & 0x7f807f80u;
+            const uint32_t pf[4] = {mul_bf16x2(pr[0], f0), mul_bf16x2(pr[1], f0), mul_bf16x2(pr[2], f1),
+                                    mul_bf16x2(pr[3], f1)};
             uint32_t b[4];                     // 16 features x slots 0-7, 8-15; the next 16
             const int r = (lane & 15) + 16 * jj, c = 2 * blk + (lane >> 4);
             ldsm4_t(b, vs + r * 128 + ((c ^ (r & 7)) << 4));
@@ -587,11 +594,13 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         }
       }
       pa_release(empty + st, lane);
+      if constexpr (kAhead) {
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
+        for (int j = 0; j < kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[j][i] = s_next[j][i];
-      mask = mask_next;
+          for (int i = 0; i < 4; ++i) s[j][i] = s_next[j][i];
+        mask = mask_next;
+      }
     }
     base_g += it.steps;
 
