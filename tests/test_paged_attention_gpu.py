@@ -315,3 +315,181 @@ def test_keys_as_values(dsa):
     out, lse = attend(dsa, c, dev, table, q.cuda(), np.array([255, 99]), SCALE)
     ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("k"), c.table, [255, 99], None, SCALE)
     check_attention(out, lse, ref)
+
+
+# ---- many query heads on a key-value head: the other kernel -------------------------
+# (more than 16 over bf16, more than 48 over fp8)
+
+@pytest.mark.parametrize("fp8,G", [(False, 17), (False, 40), (False, 128), (True, 49), (True, 128)])
+@pytest.mark.parametrize("ps,layout", [(16, "slots"), (32, "gaps"), (64, "heads"), (256, "slots")])
+def test_wide_layouts_and_lengths(dsa, ps, layout, fp8, G):
+    """Lengths around the 32-slot units and the 128-slot tiles; empty rows; a
+    position past the block table."""
+    rng = np.random.default_rng(ps + G)
+    pos = np.array([0, 15, 31, 32, 63, 127, 128, 129, 255, 3 * ps - 1, 3 * ps + 500, -1])
+    c = Cache(rng, len(pos), max(3, 320 // ps), ps, 1 if G > 64 else 2, fp8, layout)
+    run(dsa, c, queries(rng, len(pos), G * c.Hkv), pos)
+
+
+@pytest.mark.parametrize("fp8,G", [(False, 20), (True, 64)])
+@pytest.mark.parametrize("bs", [1, 2, 4, 8, 16, 32, 64, 256])
+def test_wide_blocks(dsa, bs, fp8, G):
+    rng = np.random.default_rng(bs + G)
+    pos = np.array([255, 0, 17, -1, 130, 200])
+    c = Cache(rng, len(pos), 4, 64, 2, fp8)
+    total, n = max(1, 256 // bs), max(1, 160 // bs)
+    for each in (False, True):
+        blocks = np.stack([[np.resize(rng.permutation(total + 2), n) for _ in range(2 if each else 1)]
+                           for _ in pos]).astype(np.int64)
+        blocks[rng.random(blocks.shape) < 0.15] = -1
+        for window in (0, 1, 50):
+            run(dsa, c, queries(rng, len(pos), 2 * G), pos, blocks=blocks, block_size=bs, window=window)
+
+
+@pytest.mark.parametrize("fp8,G", [(False, 64), (True, 64)])
+def test_wide_split_rows_windows_and_sinks(dsa, fp8, G):
+    """Long rows shared by many CTAs, one stream or both of them without a
+    tile, short and empty rows between; windows."""
+    rng = np.random.default_rng(G)
+    c = Cache(rng, 5, 16, 256, 1, fp8)
+    pos = np.array([4095, -1, 3, 4000, 127])
+    sinks = rng.standard_normal(G)
+    q = queries(rng, 5, G)
+    run(dsa, c, q, pos, sinks=sinks)
+    for window in (1, 100, 1000):
+        run(dsa, c, q, pos, sinks=sinks, window=window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_wide_many_rows(dsa, fp8):
+    """More items than CTAs, several tokens a sequence."""
+    rng = np.random.default_rng(41)
+    c = Cache(rng, 5, 16, 32, 2, fp8)
+    T = 300
+    run(dsa, c, queries(rng, T, 2 * 50), rng.integers(-1, 512, T), seq_ids=rng.integers(0, 5, T))
+
+
+@pytest.mark.parametrize("G", [8, 64])
+@pytest.mark.parametrize("amp", [1.0, -1.0, 0.0])
+def test_growing_maximum(dsa, G, amp):
+    """Logits that grow along the slots by far more than 2^8, over several
+    tiles; a negative and a zero scale."""
+    rng = np.random.default_rng(42)
+    c = Cache(rng, 1, 16, 64, 1)
+    q = queries(rng, 1, G)
+    rows = c.rows("k")
+    flat = rows[c.table[0]].reshape(-1, D)
+    order = np.argsort((amp or 1.0) * (flat @ q[0, 0].double().numpy()))
+    rows[c.table[0]] = flat[order].reshape(16, 64, 1, D)
+    c.set_rows("k", rows)
+    run(dsa, c, q, np.array([1000]), amp=amp)
+
+
+@pytest.mark.parametrize("G", [8, 64])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_masked_slots_of_a_shared_page(dsa, G, bad):
+    """The rest of a token's last page, pages of nobody and blocks not listed
+    hold NaN or infinities."""
+    rng = np.random.default_rng(43)
+    c = Cache(rng, 2, 6, 64, 1)
+    pos = np.array([200, 5])
+    for n in ("k", "v"):
+        good, rows = c.rows(n), np.full((c.num_pages, 64, 1, D), bad)
+        for i, p in enumerate(pos):
+            for s in range(p + 1):
+                rows[c.table[i, s // 64], s % 64] = good[c.table[i, s // 64], s % 64]
+        c.set_rows(n, rows)
+    run(dsa, c, queries(rng, 2, G), pos)
+    run(dsa, c, queries(rng, 2, G), pos, window=70)
+    run(dsa, c, queries(rng, 2, G), pos, blocks=np.array([[[3, 0, 5]], [[0, 1, -1]]]), block_size=64)
+
+
+@pytest.mark.parametrize("G", [8, 64])
+def test_fp8_scales_of_every_size(dsa, G):
+    """Scale bytes from 1 to 254 in the values (with weights that keep the
+    sums finite), zero blocks, and a NaN scale, which reaches the rows that keep
+    its slot and no others."""
+    rng = np.random.default_rng(44)
+    c = Cache(rng, 3, 2, 64, 1, True)
+    data, scale = c.pools["v"]
+    per_row = scale.view(-1, 4)
+    for i, s in enumerate((1, 60, 110, 134, 135, 140, 200, 240)):
+        per_row[i::16] = s
+    per_row[8] = 0
+    data.view(-1, D)[8] = 0
+    pos = np.array([127, 100, 64])
+    q = queries(rng, 3, G)
+    run(dsa, c, q, pos)
+    # one slot of sequence 1 becomes NaN, in v and in k of another feature block
+    row = int(c.at[c.table[1, 0], 7, 0]) // D
+    data.view(-1, D)[row, 32:64] = 0
+    per_row[row, 1] = 255
+    dev, table = c.to("cuda")
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE)
+    assert torch.isnan(out[1, :, 32:64]).all() and torch.isfinite(lse).all()
+    other = torch.ones(D, dtype=torch.bool)
+    other[32:64] = False
+    assert torch.isfinite(out[1][:, other.cuda()]).all() and torch.isfinite(out[[0, 2]]).all()
+    kd, ks = c.pools["k"]
+    kd.view(-1, D)[row, :32] = 0
+    ks.view(-1, 4)[row, 0] = 255
+    dev, table = c.to("cuda")
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE)
+    assert torch.isnan(out[1]).all() and torch.isfinite(out[[0, 2]]).all()
+    out, _ = attend(dsa, c, dev, table, q.cuda(), np.array([127, 6, 64]), SCALE)
+    assert torch.isfinite(out).all()                     # slot 7 not kept
+
+
+@pytest.mark.parametrize("H,fp8", [(4, False), (40, False), (4, True), (64, True)])
+def test_again_and_again_between_other_calls(dsa, H, fp8):
+    """Many short items a CTA, so that every buffer is filled many times over;
+    between the runs a call whose keys and values are NaN goes through the same
+    shared memory. The same bits every time, and right."""
+    rng = np.random.default_rng(45)
+    c = Cache(rng, 7, 8, 16, 2, fp8)
+    T = 500
+    seq, pos = rng.integers(0, 7, T), rng.integers(-1, 128, T)
+    q = queries(rng, T, 2 * H)
+    first = run(dsa, c, q, pos, seq_ids=seq)
+    nan = Cache(rng, 40, 4, 64, 2, fill=float("nan"))
+    ndev, ntable = nan.to("cuda")
+    nq = queries(rng, 40, 2 * H).cuda()
+    dev, table = c.to("cuda")
+    qc = q.cuda()
+    desc = dsa.make_paged_attention_desc(c.desc(dsa, table), T, 2 * H, SCALE)
+    ndesc = dsa.make_paged_attention_desc(nan.desc(dsa, ntable), 40, 2 * H, SCALE)
+    n = max(dsa.dsa_paged_attention_workspace_size(d) for d in (desc, ndesc))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    out, lse, nout = torch.zeros_like(first[0]), torch.zeros_like(first[1]), torch.zeros_like(nq)
+    dpos, dseq, npos = dev_i32(pos), dev_i32(seq), dev_i32([255] * 40)
+    stream = torch.cuda.current_stream().cuda_stream
+    for _ in range(60):
+        dsa.dsa_paged_attention_forward(ndesc, nq, ndev["k"][0], None, ndev["v"][0], None, None, npos, None,
+                                        nout, None, ws, n, stream)
+        out.zero_()
+        dsa.dsa_paged_attention_forward(desc, qc, *dev["k"], *dev["v"], None, dpos, dseq, out, lse, ws, n, stream)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert dsa.dsa_indexer_get_error(ws) == dsa.DSA_OK
+
+
+@pytest.mark.parametrize("H,fp8", [(8, False), (8, True), (64, False), (64, True)])
+def test_a_wait_that_runs_out_is_reported(dsa, H, fp8):
+    """With a wait limit of a nanosecond some device-side wait runs out: the
+    kernel records the timeout and exits; the next call is right."""
+    rng = np.random.default_rng(46)
+    c = Cache(rng, 4, 32, 64, 1, fp8)
+    dev, table = c.to("cuda")
+    q, pos = queries(rng, 4, H), np.array([2047, 2000, 1500, 900])
+    desc = dsa.make_paged_attention_desc(c.desc(dsa, table), 4, H, SCALE, wait_limit_ns=1)
+    n = dsa.dsa_paged_attention_workspace_size(desc)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    out = torch.zeros((4, H, D), dtype=torch.bfloat16, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    dsa.dsa_paged_attention_forward(desc, q.cuda(), *dev["k"], *dev["v"], None, dev_i32(pos), None, out, None,
+                                    ws, n, stream)
+    status = dsa.dsa_indexer_get_error(ws, stream)
+    assert status in (dsa.DSA_OK, dsa.DSA_ERR_TIMEOUT)     # OK only if nothing had to wait
+    assert dsa.dsa_indexer_get_error(ws, stream) == dsa.DSA_OK
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE, workspace=ws)
+    ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, None, SCALE)
+    check_attention(out, lse, ref)
