@@ -20,8 +20,12 @@
  *     least block_size covers the open one.
  * A slot past the block table, or in a page outside the pool, is not kept. A
  * token with no kept slot (a negative position, a sequence outside
- * [0, num_seqs), a list of -1) gets out = 0 and lse = -infinity. What masked
- * slots hold, NaN and infinities among it, has no effect.
+ * [0, num_seqs), a list of -1) gets out = 0 and lse = -infinity, as does one
+ * whose kept slots all have the logit -infinity. What masked slots hold, NaN
+ * and infinities among it, has no effect; a NaN that is kept gives NaN. A weight
+ * e^{l_s} takes part as a bf16 number relative to its row's largest (one below
+ * 2^-126 of that may count as 0); sums are fp32. An fp8 scale byte 0 (2^-127) may count
+ * as 0.
  *
  * Where the operation is defined (page titles and sections):
  *  - NeMo AutoModel optimized_kernels, sparse_attention_torch and
@@ -35,8 +39,10 @@
  * Conventions are those of dsa_indexer.h (device pointers of the current
  * device, no allocation, host-side checks before any launch, asynchronous on
  * `stream`, a workspace of one call at a time, bounded device-side waits
- * reported by dsa_indexer_get_error). Results do not depend on the order in
- * which blocks of the GPU finish: the same call gives the same bits.
+ * reported by dsa_indexer_get_error; after a reported timeout `out` and `lse`
+ * are unspecified and the workspace can be used again). Results do not depend
+ * on the order in which blocks of the GPU finish: the same call gives the same
+ * bits.
  */
 #ifndef DSA_PAGED_ATTENTION_H
 #define DSA_PAGED_ATTENTION_H
@@ -52,12 +58,13 @@ typedef struct {
   int32_t T;               /* query tokens, >= 1                                */
   int32_t H;               /* query heads: a multiple of H_kv, with
                               H / H_kv <= 128 and T * H < 2^31                  */
-  float sm_scale;          /* logit scale (finite)                              */
+  float sm_scale;          /* logit scale, |sm_scale| < 2^127                   */
   int32_t window;          /* recent slots, >= 0 (see above)                    */
   int32_t block_size;      /* block attention: slots a block, a power of two in
                               [1, 65536]; otherwise unused                      */
   int32_t num_blocks;      /* block attention: list entries, >= 1, with
-                              num_blocks * block_size + window < 2^30           */
+                              num_blocks * block_size + window < 2^30; 0 where
+                              the descriptor serves attention over all slots    */
   int32_t block_heads;     /* block attention: 1 (one list for every head) or
                               H_kv (one for each key-value head)                */
   uint64_t wait_limit_ns;  /* device-side wait limit; 0 = the default, 4 s      */
@@ -78,8 +85,10 @@ typedef struct {
 
 /* Bytes of workspace a call needs (host only): the 256-byte header and the
  * partial results of rows whose slots are split over the GPU. 256-byte
- * aligned, zero-filled once before first use, reused freely by calls ordered
- * on one stream. */
+ * aligned, zero-filled once before first use, reused freely by attention calls
+ * (of any descriptor that it is large enough for) ordered on one stream. A
+ * descriptor with num_blocks = 0 is checked as one of attention over all
+ * slots. */
 dsa_status_t dsa_paged_attention_workspace_size(const dsa_paged_attention_desc_t *desc,
                                                 size_t *bytes);
 

@@ -18,7 +18,9 @@
  * An fp8 row holds, per 32 features, the byte e + 127 of the least power of
  * two 2^e (e >= -127) with max|x| <= 448 * 2^e, and x * 2^-e rounded to the
  * nearest e4m3, ties to even; 32 features that hold a NaN or an infinity get
- * the scale byte 255, which stands for NaN, and zero data.
+ * the scale byte 255, which stands for NaN, and zero data. An fp8 cache that
+ * other code wrote has to keep to that: NaN by the scale byte and zero data,
+ * not by e4m3's NaN codes (0x7f, 0xff).
  *
  * dsa_block_pool, per sequence i with last position p = positions[i] and
  * first new position s = start[i], for every block b of block_size slots that
@@ -76,7 +78,8 @@ typedef struct {
   dsa_kv_dtype_t dtype;    /* of the key and value pools                        */
   int64_t page_stride;     /* elements, multiples of 128, > 0: between pages,   */
   int64_t slot_stride;     /* between the slots of a page                       */
-  int64_t head_stride;     /* and between the heads of a slot                   */
+  int64_t head_stride;     /* and between the heads of a slot (for attention
+                              below 2^39)                                       */
   const int32_t *block_table; /* device [num_seqs, pages_per_seq]               */
 } dsa_paged_cache_t;
 
@@ -87,7 +90,7 @@ typedef enum {
 
 typedef struct {
   dsa_paged_cache_t cache;
-  int32_t T;               /* tokens, >= 1                                      */
+  int32_t T;               /* tokens, >= 1, with T * (H + 2 H_kv + 3) < 2^29    */
   int32_t H;               /* query heads to rotate, 0 .. 256 (0: none)         */
   int32_t rope_dim;        /* leading features turned, 0 .. D: even
                               (INTERLEAVED) or a multiple of 16 (HALVES)        */
@@ -115,7 +118,8 @@ typedef struct {
  * A position past the block table's slots, a sequence outside [0, num_seqs)
  * or a page outside the pool writes no key and no value (the token's query
  * is written all the same). Tokens of one call that name the same slot leave
- * one of their rows there, or parts of several: give each its own slot.
+ * one of their rows there, or parts of several: give each its own slot. The
+ * inputs overlap no output but for that q_out.
  */
 dsa_status_t dsa_cache_append(const dsa_append_desc_t *desc, const void *q, const void *k,
                               const void *v, const float *cos, const float *sin,
@@ -126,8 +130,8 @@ dsa_status_t dsa_cache_append(const dsa_append_desc_t *desc, const void *q, cons
 typedef struct {
   dsa_paged_cache_t cache;
   int32_t block_size;      /* slots a block, 1 .. 65536                         */
-  int64_t S_pool;          /* pooled rows per (sequence, head), >= 1: a block
-                              at or past it writes nothing                      */
+  int64_t S_pool;          /* pooled rows per (sequence, head), 1 .. 2^31 - 1:
+                              a block at or past it writes nothing              */
   int64_t seq_stride;      /* elements between sequences' pooled rows and       */
   int64_t head_stride;     /* between heads'; multiples of 128, >= 0            */
 } dsa_block_pool_desc_t;

@@ -29,7 +29,7 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
   const dsa_status_t st = check_paged_cache(&d->cache);
   if (st != DSA_OK) return st;
   if (d->T < 1 || d->H < 1 || d->H % d->cache.H_kv != 0 || d->window < 0 ||
-      !std::isfinite(d->sm_scale))
+      !std::isfinite(d->sm_scale * dsa::kPaLog2e))
     return DSA_ERR_INVALID_ARG;
   if (d->H / d->cache.H_kv > 128) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->T) * d->H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
@@ -186,6 +186,7 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
                            : (items * std::max<int64_t>(1, most_steps) + least - 1) / least;
   const int grid = static_cast<int>(std::min(most, want));
   p.chain_by_item = items <= grid;
+  p.ctas = grid;
   const int entries = static_cast<int>(std::min<int64_t>(items, grid));
   const int variant = (plan.wide ? 4 : 0) + (plan.fp8 ? 2 : 0) + (list ? 1 : 0);
   static const AttnFn fns[8] = {

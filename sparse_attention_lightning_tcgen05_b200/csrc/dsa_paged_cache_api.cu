@@ -223,7 +223,8 @@ dsa_status_t dsa_block_pool(const dsa_block_pool_desc_t *desc, const void *k_cac
   // the kernel numbers up to kPoolSeqs sequences' items in 32 bits
   if (sets * c.H_kv > INT32_MAX / std::min(c.num_seqs, dsa::kPoolSeqs)) return DSA_ERR_UNSUPPORTED;
   const bool fp8 = c.dtype != DSA_KV_BF16;
-  const int64_t most = (sets * c.H_kv * c.num_seqs + per_cta - 1) / per_cta;
+  // (blocks larger than the table are never complete: last_block is still due)
+  const int64_t most = std::max<int64_t>(1, (sets * c.H_kv * c.num_seqs + per_cta - 1) / per_cta);
   const int wave = dev->num_sms * (fp8 ? dsa::kPoolCtasPerSm<true> : dsa::kPoolCtasPerSm<false>);
   const int blocks = static_cast<int>(std::min<int64_t>(most, wave));
   p.S_pool = desc->S_pool;

@@ -609,6 +609,9 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     for (int i = 0; i < 2; ++i) {
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+      // no maximum although slots were kept, their logits being NaN: any
+      // number, so that the sum is not taken for an empty one
+      if (m[i] == neg_inf && sum[i] != 0.f) m[i] = 0.f;
     }
     const int turn = (warp - n) & (kPaWarps - 1);
     // the last item's sum is taken over (every warp waits: a wait below must
@@ -696,10 +699,11 @@ __global__ void __launch_bounds__(kPaThreads, 2)
 // a's second place and in the first place of a + 1 .. last. kWays warps a head,
 // a 4-feature piece a lane, each over every kWays-th partial with kBatch of
 // them in flight, added up through shared memory in warp order. Eight ways
-// where items are few and their partials many (37 partials of 128 heads: 20 us
-// by one warp a head and one at a time, 12 us eight at a time, 3 us so); one
-// way, and fewer blocks, where most items lie in one or two CTAs (296 CTAs'
-// entries with eight ways: 10 us, with one: 3).
+// where items are few and their partials many (4 contexts of 65,000 to 131,072
+// slots under 128 heads, 37 partials an item: the whole call 70 us by one warp a
+// head, 57 so); one way, and fewer blocks, where most items lie in one or two
+// CTAs (16 contexts of 2,048 to 32,768 slots, 8 key heads: 185 us by eight ways,
+// 178 by one).
 constexpr int kPaJoinThreads = 512;
 template <int kWays>
 constexpr int kPaJoinHeads = kPaJoinThreads / 32 / kWays;     // of a block
@@ -717,7 +721,9 @@ __global__ void __launch_bounds__(kPaJoinThreads) paged_attention_join_kernel(
   const int head = warp / kWays, way = warp - head * kWays;
   const int r = (blockIdx.x - entry * blocks) * kPaJoinHeads<kWays> + head;
   const int4 c = p.chain[entry];
-  if (c.x < 0) return;
+  // -1: nothing to join; out of range: left by another call where a wait that
+  // ran out kept this one's entry from being written
+  if (c.x < 0 || c.x >= p.T || c.y < 0 || c.y >= p.g.H_kv * p.head_tiles || c.z < 0 || c.w >= p.ctas) return;
   const int kvh = c.y / p.head_tiles, ht = c.y - kvh * p.head_tiles;
   const bool in = r < min(p.rows, p.G - ht * p.rows);
   const float neg_inf = __int_as_float(0xff800000);

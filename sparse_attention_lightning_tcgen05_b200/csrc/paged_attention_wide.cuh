@@ -105,7 +105,6 @@ __device__ __forceinline__ void bf16_of_e4m3x16(uint4 w, uint32_t f1, uint32_t f
 
 // A slot's staged row (with its scale word) as a row of a bf16 tile.
 __device__ __forceinline__ void convert_row(const uint8_t *slot, uint32_t scales, uint8_t *tile, int r) {
-  uint32_t nan = 0;
   // two multiplications where a scale is 2^8 or more (or NaN): rare
   const bool two = ((scales & 0x7f7f7f7fu) + 0x79797979u & scales & 0x80808080u) != 0;
   uint4 in[8];                                                // (read before any store)
@@ -115,9 +114,6 @@ __device__ __forceinline__ void convert_row(const uint8_t *slot, uint32_t scales
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const uint4 w = in[c];
-    // the code 0x7f, either sign, is a NaN
-    nan |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
-           ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
     const uint32_t s = scales >> (8 * (c >> 1)) & 0xffu;
     uint32_t f1 = (s + 120u) << 7, f2 = 0;
     if (two) {
@@ -130,12 +126,6 @@ __device__ __forceinline__ void convert_row(const uint8_t *slot, uint32_t scales
     uint8_t *const row = tile + (c >> 2) * (kPwTile * 128) + r * 128;
     *reinterpret_cast<uint4 *>(row + ((((2 * c) & 7) ^ (r & 7)) << 4)) = out[0];
     *reinterpret_cast<uint4 *>(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = out[1];
-  }
-  if (nan & 0x80808080u) {
-    for (int e = 0; e < kRowD; ++e)
-      if ((slot[r * 128 + (((e >> 4) ^ (r & 7)) << 4) + (e & 15)] & 0x7f) == 0x7f)
-        *reinterpret_cast<uint16_t *>(tile + (e >> 6) * (kPwTile * 128) + r * 128 +
-                                      ((((e >> 3) & 7) ^ (r & 7)) << 4) + 2 * (e & 7)) = 0x7fc0u;
   }
 }
 
@@ -608,6 +598,7 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
         if (lane == 0) mbar_arrive(p_full + stream);
       }
       if (!ok) break;
+      if (m == neg_inf && sum != 0.f) m = 0.f;                // all kept logits NaN: not an empty row
       // ---- add the two streams up: this one writes half of the features ----
       // (once everyone has read the last item's maxima and sums)
       if (n > 0 && !pa_wait(o_free, (n - 1) & 1u, ctl, 83)) break;

@@ -40,6 +40,7 @@ struct PagedAttnParams {
   float2 *part_ml;             // [grid, 2, rows] (max in log2 units, sum)
   int4 *chain;                 // items that several CTAs share (PaChain)
   bool chain_by_item;          // an entry an item, else one a CTA
+  int ctas;                    // of the attention kernel
   unsigned int *err, *err_info;
   uint64_t wait_limit_ns, drain_limit_ns;
 };

@@ -493,3 +493,50 @@ def test_a_wait_that_runs_out_is_reported(dsa, H, fp8):
     out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE, workspace=ws)
     ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, None, SCALE)
     check_attention(out, lse, ref)
+
+
+@pytest.mark.parametrize("G,fp8", [(8, False), (64, False), (8, True), (64, True)])
+def test_a_kept_nan_gives_nan(dsa, G, fp8):
+    """Rows whose logits are all NaN (the query, or every kept key) are not
+    taken for rows without a slot, whether one CTA has them or many."""
+    rng = np.random.default_rng(47)
+    c = Cache(rng, 3, 80, 64, 1, fp8)
+    if fp8:
+        data, scale = c.pools["k"]
+        idx = c.at[c.table[1, 0], 0, 0]
+        data[idx:idx + 32], scale[idx // 32] = 0, 255
+    else:
+        rows = c.rows("k")
+        rows[c.table[1, 0], 0, 0, 5] = np.nan
+        c.set_rows("k", rows)
+    dev, table = c.to("cuda")
+    q = queries(rng, 3, G)
+    q[2, 1::2, 7] = float("nan")
+    out, lse = attend(dsa, c, dev, table, q.cuda(), np.array([100, 0, 5100]), SCALE)
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.isnan(out[2, 1::2]).all() and torch.isnan(lse[2, 1::2]).all()
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2, ::2]).all() and torch.isfinite(lse[2, ::2]).all()
+    out, lse = attend(dsa, c, dev, table, q.cuda(), np.array([100, 0, 5100]), SCALE,
+                      blocks=np.array([[[0]], [[0]], [[1]]]), block_size=64)
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all() and torch.isnan(lse[2, 1::2]).all()
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2, ::2]).all()
+
+
+@pytest.mark.parametrize("H", [8, 64])
+def test_a_timeout_writes_no_row_of_another_call(dsa, H):
+    """Where waits run out, what an earlier and larger call left in the
+    workspace leads to no write past this call's rows."""
+    rng = np.random.default_rng(48)
+    c = Cache(rng, 4, 32, 64, 1)
+    dev, table = c.to("cuda")
+    q, pos = queries(rng, 4, H).cuda(), dev_i32([2047, 2000, 1500, 900])
+    desc = dsa.make_paged_attention_desc(c.desc(dsa, table), 4, H, SCALE, wait_limit_ns=1)
+    n = dsa.dsa_paged_attention_workspace_size(desc)
+    stream = torch.cuda.current_stream().cuda_stream
+    for fill in (1, 5, 0x70):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        out = torch.full((64, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        dsa.dsa_paged_attention_forward(desc, q, *dev["k"], *dev["v"], None, pos, None, out, None, ws, n, stream)
+        assert dsa.dsa_indexer_get_error(ws, stream) in (dsa.DSA_OK, dsa.DSA_ERR_TIMEOUT)
+        assert torch.all(out[4:] == 7.0)

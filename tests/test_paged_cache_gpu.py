@@ -292,6 +292,14 @@ def test_pool_one_large_block(dsa):
     run_pool(dsa, c, 2048, 1, None, np.array([2303, 2046]))
 
 
+@pytest.mark.parametrize("bs", [33, 64, 65536])
+def test_pool_blocks_larger_than_the_table(dsa, bs):
+    """No block is ever complete; the last one is still told: -1."""
+    rng = np.random.default_rng(33)
+    c = Cache(rng, 3, 2, 16, 2, values=False)
+    assert run_pool(dsa, c, bs, 1, None, np.array([31, -1, 100])) == 0
+
+
 def test_pool_pages_outside_the_pool_count_as_zeros(dsa):
     rng = np.random.default_rng(32)
     c = Cache(rng, 2, 4, 16, 2, values=False)

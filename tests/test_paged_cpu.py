@@ -131,7 +131,8 @@ def attention(ckw=None, dkw=None, blocks=None, ws_bytes=1 << 30, **over):
 @pytest.mark.parametrize("kw,code", [
     (dict(dkw=dict(T=0)), INV), (dict(dkw=dict(H=0)), INV), (dict(dkw=dict(H=3)), INV),
     (dict(dkw=dict(H=258)), UNS), (dict(dkw=dict(T=1 << 30)), UNS), (dict(dkw=dict(sm_scale=float("inf"))), INV),
-    (dict(dkw=dict(sm_scale=float("nan"))), INV), (dict(dkw=dict(window=-1)), INV),
+    (dict(dkw=dict(sm_scale=float("nan"))), INV), (dict(dkw=dict(sm_scale=3e38)), INV),
+    (dict(dkw=dict(window=-1)), INV),
     (dict(q=None), INV), (dict(q=FAKE + 8), INV), (dict(out=None), INV), (dict(out=FAKE + 4), INV),
     (dict(positions=None), INV), (dict(positions=FAKE + 2), INV), (dict(sinks=FAKE + 2), INV),
     (dict(seq_ids=FAKE + 1), INV), (dict(lse=FAKE + 2), INV), (dict(k=None), INV), (dict(v=None), INV),
