@@ -36,8 +36,8 @@ constexpr int kPwUnit = 32;                        // slots a lookup round's uni
 constexpr int kPwRows = 128;                       // query heads of a work item, at most
 constexpr int kPwLeast = 2;                        // tiles worth a CTA
 constexpr int kPwMmaWarp = 8;
-constexpr int kPwConvertWarp = 10;                 // fp8: and the next
-constexpr int kPwConvertWarps = 2;
+constexpr int kPwConvertWarp = 10;                 // fp8: and the next five
+constexpr int kPwConvertWarps = 6;
 
 // Shared memory: bf16 tiles as two halves of their rows ([128 x 128 bytes]
 // each, 128-byte swizzle), loaded directly or (fp8) converted from slots of a
@@ -84,6 +84,16 @@ __device__ __forceinline__ void st_global_v8(float *dst, const float *v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]),
                "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+// This thread's lane of 16 TMEM columns from taddr on.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
 }
 
 // 16 e4m3 features of a row as 16 bf16 values times a power of two: f1 is
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
   int *const start_row = reinterpret_cast<int *>(info + 1) + 1;
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(info + 1) + 2;
   int64_t *const start_step = reinterpret_cast<int64_t *>(smem + Smem::off_misc + 32);
-  int64_t *const scan = start_step + 1;                             // [10]
+  int64_t *const scan = start_step + 1;                             // [kThreads / 32]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kPwMmaWarp) {
@@ -207,8 +217,10 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
   if (range.begin >= range.end) {
     PaChain{}.finish(p, tid);
   } else if (kFp8 && warp >= kPwConvertWarp) {
-    // ---------------- conversion: a slot's row a thread at a time ----------------
-    const int r0 = tid - kPwConvertWarp * 32;
+    // ---------------- conversion: a unit a warp, a slot's row a thread ----------------
+    // units in turn, so that six warps share the four of a load evenly; every
+    // warp waits and arrives for every load, so that none is a phase apart
+    int sub = warp - kPwConvertWarp;                          // this warp's unit, from the load's first
     const uint32_t tiles = static_cast<uint32_t>(range.end - range.begin);
     for (uint32_t c = 0; c < 2 * tiles; ++c) {
       const uint32_t t = c >> 1, is_v = c & 1u;
@@ -220,8 +232,9 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
       const uint8_t *const from = smem + Smem::off_slot + slot * Smem::kSlotBytes;
       uint8_t *const to = smem + (is_v ? Smem::off_v : Smem::off_k) + st * Smem::kTileBytes;
       const uint32_t *const scales = reinterpret_cast<const uint32_t *>(smem + Smem::off_scale) + slot * kPwTile;
-      for (int r = r0; r < kPwTile; r += kPwConvertWarps * 32) {
-        if (masks[t % Smem::kMasks * kSub + (r >> 5)] >> (r & 31) & 1u) {
+      if (sub < kSub) {
+        const int r = sub * kPwUnit + lane;
+        if (masks[t % Smem::kMasks * kSub + sub] >> lane & 1u) {
           convert_row(from, scales[r], to, r);
         } else {
           // a slot that is not kept: whatever was staged, its row is zero
@@ -230,7 +243,9 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
             *reinterpret_cast<uint4 *>(to + (i >> 3) * Smem::kHalf + r * 128 + ((i & 7) << 4)) =
                 make_uint4(0u, 0u, 0u, 0u);
         }
+        sub += kPwConvertWarps;
       }
+      sub -= kSub;
       pa_release((is_v ? v_full : k_full) + st, lane);        // read by the products (async proxy)
       if (lane == 0) mbar_arrive(slot_empty + slot);
     }
@@ -491,8 +506,9 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
       bool first = true;
       for (int i = (stream ^ g) & 1; i < it.steps; i += 2) {
         const uint32_t t = g + i, st = t % kVStages, mt = t % Smem::kMasks * kSub;
+        // (bf16: V's tile too, for the rows zeroed below)
         if (!pa_wait(s_full + stream, (t >> 1) & 1u, ctl, 78) ||
-            !pa_wait(v_full + st, (t / kVStages) & 1u, ctl, 79)) {
+            (!kFp8 && !pa_wait(v_full + st, (t / kVStages) & 1u, ctl, 79))) {
           ok = false;
           break;
         }
@@ -563,30 +579,26 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
           }
           float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float pk[32];
+          for (int q4 = 0; q4 < 4; ++q4) {
+            float pk[16];
+            float (&x)[32] = v[q4 & 1];
+            tmem_wait_ld32(x);
+            if (q4 < 3) ahead(q4 + 1);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int q4 = 2 * half + q;
-              float (&x)[32] = v[q4 & 1];
-              tmem_wait_ld32(x);
-              if (q4 < 3) ahead(q4 + 1);
+            for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
+            if (!every) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
-              if (!every) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(mw[q4] >> c & 1u)) x[c] = neg_inf;
-              }
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float e0 = ex2_approx(x[2 * c]), e1 = ex2_approx(x[2 * c + 1]);
-                s4[c & 3] += e0 + e1;
-                pk[16 * q + c] = __uint_as_float(pack_bf16x2(e0, e1));
-              }
+              for (int c = 0; c < 32; ++c)
+                if (!(mw[q4] >> c & 1u)) x[c] = neg_inf;
             }
-            // columns 32 half .. + 31: their logits have been read twice
-            tmem_st32(t_s + 32 * half, pk);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float e0 = ex2_approx(x[2 * c]), e1 = ex2_approx(x[2 * c + 1]);
+              s4[c & 3] += e0 + e1;
+              pk[c] = __uint_as_float(pack_bf16x2(e0, e1));
+            }
+            // columns 16 q4 .. + 15: their logits have been read twice
+            tmem_st16(t_s + 16 * q4, pk);
           }
           sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
           tmem_wait_st();
