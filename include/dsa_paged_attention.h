@@ -24,8 +24,7 @@
  * whose kept slots all have the logit -infinity. What masked slots hold, NaN
  * and infinities among it, has no effect; a NaN that is kept gives NaN. A weight
  * e^{l_s} takes part as a bf16 number relative to its row's largest (one below
- * 2^-126 of that may count as 0); sums are fp32. An fp8 scale byte 0 (2^-127) may count
- * as 0.
+ * 2^-126 of that may count as 0); sums are fp32.
  *
  * Where the operation is defined (page titles and sections):
  *  - NeMo AutoModel optimized_kernels, sparse_attention_torch and

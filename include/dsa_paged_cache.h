@@ -20,7 +20,7 @@
  * nearest e4m3, ties to even; 32 features that hold a NaN or an infinity get
  * the scale byte 255, which stands for NaN, and zero data. An fp8 cache that
  * other code wrote has to keep to that: NaN by the scale byte and zero data,
- * not by e4m3's NaN codes (0x7f, 0xff).
+ * not by e4m3's NaN codes (0x7f, 0xff). A scale byte 0 (2^-127) may be read as 0.
  *
  * dsa_block_pool, per sequence i with last position p = positions[i] and
  * first new position s = start[i], for every block b of block_size slots that

@@ -132,9 +132,6 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   p.rows = plan.rows;
   p.head_tiles = plan.head_tiles;
   p.window = d->window;
-  // tokens that share a sequence read the same slots: head by head, so that one
-  // head's slots stay in L2 while all its tokens pass
-  p.head_major = p.T > p.g.num_seqs;
   const int unit = std::min(plan.step, 32);
   int unit_shift = unit == 32 ? 5 : 4;
   int64_t most_steps = (p.g.capacity() + plan.step - 1) / plan.step;
@@ -178,13 +175,21 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
     if (st != DSA_OK) return st;
   }
   // no more CTAs than have enough steps
-  const int least = plan.wide ? dsa::kPwLeast : dsa::kPaLeast;
+  const int least = plan.wide  ? dsa::kPwLeast
+                    : plan.fp8 ? dsa::PaSmem<true>::kLeast
+                               : dsa::PaSmem<false>::kLeast;
   const int64_t items = static_cast<int64_t>(p.T) * p.g.H_kv * p.head_tiles;
   const int64_t most = std::min(plan.grid, dev->num_sms * (plan.wide ? 1 : kPaCtasPerSm));
   const int64_t want = items > most * least
                            ? most
                            : (items * std::max<int64_t>(1, most_steps) + least - 1) / least;
-  const int grid = static_cast<int>(std::min(most, want));
+  int grid = static_cast<int>(std::min(most, want));
+  // A multiple of the key heads, where that idles less than a sixteenth of the
+  // CTAs: the heads' shares then begin alike, and what lies side by side in
+  // memory (a slot's rows and scales of all heads) is read at the same time. 64
+  // contexts of 1,024 to 32,768 slots, 4 key heads, fp8: 251 us otherwise, 243 so;
+  // 16 contexts, 8 key heads, bf16: 179 and 173.
+  if (grid % p.g.H_kv * 16 < grid) grid -= grid % p.g.H_kv;
   p.chain_by_item = items <= grid;
   p.ctas = grid;
   const int entries = static_cast<int>(std::min<int64_t>(items, grid));
@@ -196,8 +201,8 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
       dsa::paged_attention_wide_kernel<true, false>,  dsa::paged_attention_wide_kernel<true, true>};
   static const int smems[4] = {dsa::PaSmem<false>::kTotal, dsa::PaSmem<true>::kTotal,
                                dsa::PwSmem<false>::kTotal, dsa::PwSmem<true>::kTotal};
-  static const int threads_of[4] = {dsa::kPaThreads, dsa::kPaThreads, dsa::PwSmem<false>::kThreads,
-                                    dsa::PwSmem<true>::kThreads};
+  static const int threads_of[4] = {dsa::PaSmem<false>::kThreads, dsa::PaSmem<true>::kThreads,
+                                    dsa::PwSmem<false>::kThreads, dsa::PwSmem<true>::kThreads};
   const int smem = smems[variant >> 1], threads = threads_of[variant >> 1];
   st = ensure_smem_attr(dev, kAttrPagedAttn + variant, fns[variant], smem);
   if (st != DSA_OK) return st;

@@ -23,10 +23,7 @@
 
 namespace dsa {
 
-constexpr int kPaWarps = 4;                        // consumer warps
-constexpr int kPaThreads = (kPaWarps + 1) * 32;    // and the producer
 constexpr int kPaRows = 16;                        // query heads of a work item
-constexpr int kPaLeast = 2 * kPaWarps;             // steps worth a CTA
 
 __device__ __forceinline__ void cp_async4_zfill(void *smem_dst, const void *gmem_src,
                                                 uint32_t src_bytes) {
@@ -116,9 +113,12 @@ struct PaItem {
 template <bool kFp8>
 struct PaSmem {
   static constexpr int kStep = kFp8 ? 32 : 16;
+  static constexpr int kWarps = kFp8 ? 5 : 4;                       // consumer warps
+  static constexpr int kThreads = (kWarps + 1) * 32;                // and the producer
+  static constexpr int kLeast = 2 * kWarps;                         // steps worth a CTA
   // three a consumer warp; a stage is always the same warp's, so that no warp
   // waits for a phase before the last one of its barrier is over
-  static constexpr int kStages = 3 * kPaWarps;
+  static constexpr int kStages = (kFp8 ? 2 : 3) * kWarps;
   static constexpr int kBox = kStep * 128;                          // one [kStep x 128 B] box
   static constexpr int kBoxes = kFp8 ? 1 : 2;                       // of a row
   static constexpr int off_v = kBoxes * kBox;
@@ -144,25 +144,25 @@ struct PaSmem {
 // none waits long); the last one writes. Items that lie in one CTA are finished
 // here; of the others each CTA leaves a partial result for the join kernel.
 template <bool kFp8, bool kList>
-__global__ void __launch_bounds__(kPaThreads, 2)
+__global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                            const __grid_constant__ CUtensorMap tmap_k,
                            const __grid_constant__ CUtensorMap tmap_v, const PagedAttnParams p) {
   using Smem = PaSmem<kFp8>;
-  constexpr int kStep = Smem::kStep;
+  constexpr int kStep = Smem::kStep, kWarps = Smem::kWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t *const masks = reinterpret_cast<uint32_t *>(smem + Smem::off_mask);
   uint64_t *const full = reinterpret_cast<uint64_t *>(smem + Smem::off_bar);
   uint64_t *const empty = full + Smem::kStages;
   uint64_t *const q_full = empty + Smem::kStages;
   uint64_t *const q_empty = q_full + 1;
-  uint64_t *const hand_full = q_empty + 1;                          // [kPaWarps - 1]
-  uint64_t *const hand_empty = hand_full + kPaWarps - 1;
+  uint64_t *const hand_full = q_empty + 1;                          // [kWarps - 1]
+  uint64_t *const hand_empty = hand_full + kWarps - 1;
   PaItem *const info = reinterpret_cast<PaItem *>(smem + Smem::off_misc);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(info + 1);
   int *const start_row = reinterpret_cast<int *>(info + 1) + 1;
   int64_t *const start_step = reinterpret_cast<int64_t *>(smem + Smem::off_misc + 32);
-  int64_t *const scan = start_step + 1;                             // [kPaWarps + 1]
+  int64_t *const scan = start_step + 1;                             // [kWarps + 1]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       mbar_init(empty + i, 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, kPaWarps);
-    for (int i = 0; i < kPaWarps - 1; ++i) mbar_init(hand_full + i, 1);
+    mbar_init(q_empty, kWarps);
+    for (int i = 0; i < kWarps - 1; ++i) mbar_init(hand_full + i, 1);
     mbar_init(hand_empty, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -183,17 +183,17 @@ __global__ void __launch_bounds__(kPaThreads, 2)
   grid_dep_wait();
   grid_dep_launch_dependents();
   const PaRange range =
-      pa_range<kList, kStep, kPaThreads>(p, kPaLeast, tid, scan, start_row, start_step);
+      pa_range<kList, kStep, Smem::kThreads>(p, Smem::kLeast, tid, scan, start_row, start_step);
   if (range.begin >= range.end) {
     PaChain{}.finish(p, tid);
     return;
   }
   const WaitCtl ctl{abort_flag, p.err, p.err_info, p.wait_limit_ns};
 
-  if (warp == kPaWarps) {
+  if (warp == kWarps) {
     // ---------------- producer ----------------
     PaCursor<kList, kStep> cur;
-    cur.start(p, range.outer, *start_row, *start_step, range.end - range.begin);
+    cur.start(p, range.kvh, *start_row, *start_step, range.end - range.begin);
     PaLookup<kList, kStep, kStep> look;
     look.start(p, lane, cur);
     PaChain chain;
@@ -476,11 +476,11 @@ __global__ void __launch_bounds__(kPaThreads, 2)
     constexpr bool kAhead = !kFp8;                            // fp8: no registers for it
     float s[kJ][4], s_next[kAhead ? kJ : 1][4];
     uint32_t mask = 0, mask_next = 0;
-    const int step0 = (warp - base_g) & (kPaWarps - 1);
+    const int step0 = static_cast<int>((warp + kWarps - base_g % kWarps) % kWarps);
     if (kAhead && step0 < it.steps && !logits(base_g + step0, s, mask)) return;
-    for (int step = step0; step < it.steps; step += kPaWarps) {
+    for (int step = step0; step < it.steps; step += kWarps) {
       if constexpr (kAhead) {
-        if (step + kPaWarps < it.steps && !logits(base_g + step + kPaWarps, s_next, mask_next)) return;
+        if (step + kWarps < it.steps && !logits(base_g + step + kWarps, s_next, mask_next)) return;
       } else {
         if (!logits(base_g + step, s, mask)) return;
       }
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
       // number, so that the sum is not taken for an empty one
       if (m[i] == neg_inf && sum[i] != 0.f) m[i] = 0.f;
     }
-    const int turn = (warp - n) & (kPaWarps - 1);
+    const int turn = static_cast<int>((warp + kWarps - n % kWarps) % kWarps);
     // the last item's sum is taken over (every warp waits: a wait below must
     // not meet the phase before)
     if (!pa_wait(hand_empty, (n & 1u) ^ 1u, ctl, 64)) return;
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kPaThreads, 2)
         for (int j = 0; j < 4; ++j)
           o[k][j] = fmaf(b[j >> 1], hand[32 * (4 + 4 * k + j)], a[j >> 1] * o[k][j]);
     }
-    if (turn < kPaWarps - 1) {
+    if (turn < kWarps - 1) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         hand[32 * i] = m[i];

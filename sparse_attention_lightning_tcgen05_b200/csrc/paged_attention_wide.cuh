@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
   } else if (warp > kPwMmaWarp) {
     // ---------------- producer ----------------
     PaCursor<kList, kPwTile> cur;
-    cur.start(p, range.outer, *start_row, *start_step, range.end - range.begin);
+    cur.start(p, range.kvh, *start_row, *start_step, range.end - range.begin);
     PaLookup<kList, kPwTile, kPwUnit> look;
     look.start(p, lane, cur);
     PaChain chain;

@@ -79,11 +79,6 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t v) {
   return make_float2(lo, hi);
 }
 
-// The value 2^(b - 127) of an e8m0 byte (255: NaN; 0: 2^-127, a denormal).
-__device__ __forceinline__ float e8m0_f32(uint32_t b) {
-  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fffffffu : b << 23);
-}
-
 // The e8m0 byte of 32 features whose largest magnitude has the bits `top`, or
 // 255 where one is a NaN or an infinity (their bits compare above every
 // number's). 448 = 1.75 * 2^8, so the least e with amax <= 448 * 2^e is
@@ -391,11 +386,13 @@ __device__ __forceinline__ PoolRaw<kFp8> pool_load(const PoolParams &p, int64_t 
   return r;
 }
 
-// acc += the row's features (fp8: under the scale byte e)
+// acc += the row's features (fp8: under the scale byte number blk of e, as an fp32
+// exponent: 0 makes 0, and 255 an infinity, which makes NaN of the zeros beside
+// it)
 template <bool kFp8>
-__device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &r, uint32_t e) {
+__device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &r, uint32_t e, int blk) {
   if constexpr (kFp8) {
-    const float f = e8m0_f32(e);
+    const float f = __uint_as_float(__byte_perm(e, 0, blk << 12 | 0x444) >> 1);
     const uint32_t q[4] = {r.w.x & 0xffffu, r.w.x >> 16, r.w.y & 0xffffu, r.w.y >> 16};
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = ffma2(e4m3x2_f32(q[i]), make_float2(f, f), acc[i]);
@@ -531,8 +528,8 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
 #pragma unroll
           for (int u = 0; u < kPoolRun; ++u) {
             uint32_t e = 0;
-            if constexpr (kFp8) e = __shfl_sync(0xffffffffu, sc, u, kPoolLanes) >> (8 * (l >> 2)) & 0xffu;
-            pool_add<kFp8>(acc, w[u], e);
+            if constexpr (kFp8) e = __shfl_sync(0xffffffffu, sc, u, kPoolLanes);
+            pool_add<kFp8>(acc, w[u], e, l >> 2);
             if (kR < 16 && u % (kR > 0 ? kR : 1) == kR - 1) {
               // a block ends; its size is a power of two: the product is the quotient
               const int b = cur.b0 + u / (kR > 0 ? kR : 1);
@@ -568,7 +565,7 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
             }
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) pool_add<kFp8>(acc, w[u], e[u]);
+          for (int u = 0; u < 4; ++u) pool_add<kFp8>(acc, w[u], e[u], 0);
         }
         next = locate(it0 + per_cta + mine);
       }

@@ -29,7 +29,6 @@ struct PagedAttnParams {
   int block_shift, num_blocks, block_heads;
   int gran_shift;              // log2 of the slots one lookup and one box cover
   int list_steps;              // steps that the listed blocks take
-  bool head_major;             // items by key-value head, then token; else by token
   float scale_log2;
   const uint8_t *k_scale, *v_scale;
   const float *sinks;
@@ -45,17 +44,14 @@ struct PagedAttnParams {
   uint64_t wait_limit_ns, drain_limit_ns;
 };
 
-// Where the items are in a CTA's order, (head, token, head tile) or (token,
-// head, head tile): `outer` groups of T rows of `inner` items each.
-__device__ __forceinline__ int pa_inner(const PagedAttnParams &p) {
-  return p.head_major ? p.head_tiles : p.g.H_kv * p.head_tiles;
-}
+// The items' order is (key-value head, token, tile of query heads): tokens of one
+// sequence read the same slots, and one head's stay in L2 while they pass.
 
 // A CTA's range of all items' steps, [begin, end) of `total`, one of `ctas` that
-// have any; and the group of items it starts in.
+// have any; and the key-value head it starts in.
 struct PaRange {
   int64_t begin, end, total, ctas;
-  int outer;
+  int kvh;
 };
 
 // The entries that tell the join kernel which items several CTAs share, written
@@ -119,7 +115,7 @@ __device__ __forceinline__ PaRow pa_row(const PagedAttnParams &p, int t) {
 // next row's position is loaded one row ahead.
 template <bool kList, int kStep>
 struct PaCursor {
-  int outer, t, item;          // item: of the row, below pa_inner
+  int kvh, t, item;          // key-value head, token, tile
   int first, steps;            // 0 steps: the range is over
   int64_t left;                // steps to the range's end, this item's among them
   PaRow row;
@@ -130,10 +126,10 @@ struct PaCursor {
     next_seq = p.seq_ids ? __ldg(p.seq_ids + n) : n;
     next_pos = __ldg(p.positions + n);
   }
-  // `offset` steps into row t of group `outer`, for `count` steps
-  __device__ __forceinline__ void start(const PagedAttnParams &p, int outer_, int t_, int64_t offset,
+  // `offset` steps into row t of head `kvh`, for `count` steps
+  __device__ __forceinline__ void start(const PagedAttnParams &p, int kvh_, int t_, int64_t offset,
                                         int64_t count) {
-    outer = outer_;
+    kvh = kvh_;
     t = t_;
     row = pa_row<kList, kStep>(p, t);
     fetch(p);
@@ -145,11 +141,11 @@ struct PaCursor {
   __device__ __forceinline__ void advance(const PagedAttnParams &p) {
     left -= steps;
     first = 0;
-    if (left > 0 && ++item == pa_inner(p)) {
+    if (left > 0 && ++item == p.head_tiles) {
       item = 0;
       if (++t == p.T) {
         t = 0;
-        ++outer;
+        ++kvh;
       }
       row = pa_row_of<kList, kStep>(p, next_seq, next_pos);
       fetch(p);
@@ -158,7 +154,7 @@ struct PaCursor {
   }
   // of the row's H_kv * head_tiles items
   __device__ __forceinline__ int id(const PagedAttnParams &p) const {
-    return p.head_major ? outer * p.head_tiles + item : item;
+    return kvh * p.head_tiles + item;
   }
 };
 
@@ -201,7 +197,7 @@ struct PaLookup {
     e_block = -1;
     if (kList && e_unit >= 0 && e_unit < p.list_steps * kSub) {
       const int e = (e_unit * kUnit + within(p, lane)) >> p.block_shift;
-      const int list = cur.t * p.block_heads + (p.block_heads > 1 ? cur.id(p) / p.head_tiles : 0);
+      const int list = cur.t * p.block_heads + (p.block_heads > 1 ? cur.kvh : 0);
       if (e < p.num_blocks) e_block = __ldg(p.blocks + static_cast<int64_t>(list) * p.num_blocks + e);
     }
     sub += batch(p);
@@ -259,7 +255,7 @@ __device__ __forceinline__ PaRange pa_range(const PagedAttnParams &p, int least,
                                             int *start_row, int64_t *start_step) {
   constexpr int kWarps = kThreads / 32;
   const int lane = tid & 31, warp = tid >> 5;
-  const int inner = pa_inner(p), groups = p.head_major ? p.g.H_kv : 1;
+  const int inner = p.head_tiles;
   const int per = (p.T + kThreads - 1) / kThreads;
   const int ra = min(p.T, tid * per), rb = min(p.T, ra + per);
   int64_t mine = 0;
@@ -280,15 +276,15 @@ __device__ __forceinline__ PaRange pa_range(const PagedAttnParams &p, int least,
   }
   group *= inner;
   PaRange r;
-  r.total = group * groups;
+  r.total = group * p.g.H_kv;
   // no more CTAs than get `least` steps, and the working ones are the first
   // ones, so that an item's CTAs follow one another
   r.ctas = min(static_cast<int64_t>(gridDim.x), (r.total + least - 1) / least);
   const bool in = blockIdx.x < r.ctas;
   r.begin = in ? r.total * blockIdx.x / r.ctas : r.total;
   r.end = in ? r.total * (blockIdx.x + 1) / r.ctas : r.total;
-  r.outer = in ? static_cast<int>(r.begin / group) : 0;
-  const int64_t at = r.begin - r.outer * group;
+  r.kvh = in ? static_cast<int>(r.begin / group) : 0;
+  const int64_t at = r.begin - r.kvh * group;
   const int64_t excl = (before + incl - mine) * inner;
   if (r.begin < r.end && at >= excl && at < (before + incl) * inner) {
     int64_t x = excl;
