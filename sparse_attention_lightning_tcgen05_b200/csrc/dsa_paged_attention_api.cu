@@ -50,11 +50,16 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
 // The kernel of a call. Wide: all query heads of a key-value head as the rows of
 // one tcgen05 tile, from more than 16 of them on (the other kernel takes 16 at a
 // time, each time with all the slots), for an fp8 cache from more than 48 on:
-// there the wide kernel's conversion bounds it whatever the heads. Four contexts
-// of 65,536 slots, one key head, us, other kernel / wide:
-//   heads        16         32         64        128
-//   bf16     32 / 34    36 / 35    59 / 37   108 / 39
-//   fp8      29 / 64    45 / 64    76 / 66   140 / 70
+// there the conversion bounds the wide kernel whatever the heads. Contexts with
+// one key head, us, other kernel / wide:
+//   heads               16         32         48         64        128
+//   bf16 4 x 65,536  32 / 35    36 / 35    68 / 36    59 / 37   109 / 39
+//        16 x 4,096  14 / 23    19 / 23    21 / 25    24 / 26    32 / 31
+//   fp8  4 x 65,536  24 / 53    35 / 53    49 / 54    60 / 54   110 / 55
+//        16 x 4,096  18 / 31    22 / 32    24 / 33    27 / 35    39 / 39
+// Lengths are not known on the host; what the wide kernel loses on short
+// contexts is a few us, what it gains on many long ones is the larger part (64
+// contexts of 1,024 to 32,768 slots, 2 key heads of 32 heads, bf16: 315 / 194).
 struct Plan {
   bool fp8, wide;
   int rows, head_tiles, step, grid;      // grid: CTAs at most

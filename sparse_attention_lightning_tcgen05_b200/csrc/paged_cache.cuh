@@ -3,11 +3,12 @@
 // fp8), and the mean key of every completed block.
 //
 // Both move each byte once and compute next to nothing, so memory bounds the
-// long calls and the launch the short ones; what they spend instructions on
-// is the fp8 format (a maximum, a scale and a conversion per feature). A head
-// row (128 features) lies across 8 or 16 neighbouring lanes: the rotation's
-// partner features sit in the same lane (interleaved pairs) or a fixed number
-// of lanes away (halves), and so do the 32 features of an e8m0 scale.
+// long bf16 calls and the launch the short ones; the fp8 format (a maximum, a
+// scale and a conversion per feature) makes the long fp8 calls bound by
+// instructions. A head row (128 features) lies across 8 or 16 neighbouring
+// lanes: the rotation's partner features sit in the same lane (interleaved
+// pairs) or a fixed number of lanes away (halves), and so do the 32 features of
+// an e8m0 scale.
 #pragma once
 
 #include <cstdint>
@@ -164,8 +165,12 @@ template <bool kFp8>
 constexpr int kAppendLanes = kFp8 ? 8 : 16;
 
 // A group of lanes takes kAppendRows head rows of one token, whose cosines and
-// sines it reads once. Products and sums of the rotation are rounded one by
-// one (no fma), so that the result is the formula's in fp32.
+// sines it reads once; four rows' loads are in flight a lane. Products and sums
+// of the rotation are rounded one by one (no fma), so that the result is the
+// formula's in fp32. Measured on a B200: 16 tokens (64 query heads, 8 key heads)
+// 2.5 us, a launch; 8,192 tokens bf16 64 us, 5.3 TB/s (copying reaches 6.6);
+// 12,345 tokens' 64 query heads and one key head to fp8 71 us, 4.4 TB/s, bound by
+// instructions (one group of 16 features a lane costs about 60).
 template <bool kQFp8, bool kKvFp8, bool kHalves>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
   constexpr int kLanes = kAppendLanes<kQFp8 || kKvFp8>;
@@ -415,7 +420,10 @@ __device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &
 // item's run up meanwhile: 16 / kR blocks, or 1/16 of a larger block's rows and
 // on, which `share` half warps sum and the first of them joins (in order, so
 // that the result does not depend on timing). kR = 0: any block size, each row
-// looked up by itself.
+// looked up by itself, four in flight. Measured on a B200: a step of 64 sequences
+// 5.5 us (the chain start, positions, table, row); 240,000 bf16 keys by fours 12.2
+// us, 6.5 TB/s; 1.1 million fp8 rows by 64s 44 us, 3.2 TB/s, bound by instructions
+// (four conversions to f16x2, eight to fp32 and four packed fmas a lane and row).
 template <bool kFp8, int kR>
 __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
     block_pool_kernel(const PoolParams p) {

@@ -115,7 +115,7 @@ __device__ __forceinline__ PaRow pa_row(const PagedAttnParams &p, int t) {
 // next row's position is loaded one row ahead.
 template <bool kList, int kStep>
 struct PaCursor {
-  int kvh, t, item;          // key-value head, token, tile
+  int kvh, t, item;            // key-value head, token, tile
   int first, steps;            // 0 steps: the range is over
   int64_t left;                // steps to the range's end, this item's among them
   PaRow row;
