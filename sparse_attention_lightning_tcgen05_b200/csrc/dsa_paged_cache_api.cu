@@ -217,9 +217,10 @@ dsa_status_t dsa_block_pool(const dsa_block_pool_desc_t *desc, const void *k_cac
   const bool pow2 = (p.block_size & (p.block_size - 1)) == 0;
   p.share = 1;
   while (p.share < dsa::kPoolGroups && p.share * dsa::kPoolRun < p.block_size) p.share *= 2;
-  p.together = pow2 ? std::max(1, dsa::kPoolRun / p.block_size) : 1;
+  p.block_shift = __builtin_ctz(static_cast<unsigned>(p.block_size));
+  const int together = pow2 ? std::max(1, dsa::kPoolRun / p.block_size) : 1;   // blocks of an item
   const int per_cta = dsa::kPoolGroups / p.share;
-  const int64_t sets = (p.g.capacity() / p.block_size + p.together - 1) / p.together;
+  const int64_t sets = (p.g.capacity() / p.block_size + together - 1) / together;
   // the kernel numbers up to kPoolSeqs sequences' items in 32 bits
   if (sets * c.H_kv > INT32_MAX / std::min(c.num_seqs, dsa::kPoolSeqs)) return DSA_ERR_UNSUPPORTED;
   const bool fp8 = c.dtype != DSA_KV_BF16;

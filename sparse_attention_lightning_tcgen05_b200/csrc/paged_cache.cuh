@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 struct PoolParams {
   PagedGeom g;
   int block_size;
+  int block_shift;           // log2 of it, where it is a power of two
   int share;                 // half warps that sum one pooled row (1 .. kPoolGroups, a power of two)
-  int together;              // blocks of an item: 16 slots' (1 where share > 1)
   int64_t S_pool, seq_stride, head_stride;
   const void *k;
   const uint8_t *k_scale;
@@ -362,12 +362,14 @@ __device__ __forceinline__ void pool_store(const float (&x)[8], const PoolParams
 }
 
 // First fresh block of a sequence, and one past the last to write.
+template <bool kPow2>
 __device__ __forceinline__ int2 pool_range(const PoolParams &p, int seq, int &done) {
   const int cap = static_cast<int>(p.g.capacity());
   const int pos = __ldg(p.positions + seq);
-  const int n = pos < cap ? pos + 1 : cap;                  // slots held
-  done = n > 0 ? n / p.block_size : 0;
-  const int first = p.start ? max(0, __ldg(p.start + seq)) / p.block_size : 0;
+  const int n = max(0, pos < cap ? pos + 1 : cap);          // slots held
+  done = kPow2 ? n >> p.block_shift : n / p.block_size;
+  const int start = p.start ? max(0, __ldg(p.start + seq)) : 0;
+  const int first = kPow2 ? start >> p.block_shift : start / p.block_size;
   return make_int2(first, static_cast<int>(min(static_cast<int64_t>(done), p.S_pool)));
 }
 
@@ -427,7 +429,8 @@ __device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &
 template <bool kFp8, int kR>
 __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
     block_pool_kernel(const PoolParams p) {
-  __shared__ float part[kPoolGroups][kRowD];
+  constexpr int kTogether = kR > 0 ? kPoolRun / (kR > 0 ? kR : 1) : 1;   // blocks of an item
+  __shared__ float4 part[2][kPoolGroups][2][kPoolLanes];    // (turns take one after the other)
   __shared__ uint32_t ends[kPoolSeqs];                      // items up to and with a sequence's
   __shared__ uint32_t warp_sum[kPoolThreads / 32];
   grid_dep_wait();
@@ -435,7 +438,9 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
   const int l = threadIdx.x & (kPoolLanes - 1), grp = threadIdx.x / kPoolLanes;
   const int per_cta = kPoolGroups / p.share;
   const int mine = grp / p.share, part_of = grp - mine * p.share;
-  const float size = static_cast<float>(p.block_size);
+  const bool warp_joins = (grp & ~1 & (p.share - 1)) == 0;  // a first half warp is in this warp
+  const float size = static_cast<float>(p.block_size), inv = 1.f / size;
+  int turn = 0;
   for (int seq0 = 0; seq0 < p.g.num_seqs; seq0 += kPoolSeqs) {
     const int seqs = min(kPoolSeqs, p.g.num_seqs - seq0);
     // ---- items of each sequence, summed up: four sequences a thread ----
@@ -447,10 +452,10 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
       int done = 0;
       count[i] = 0;
       if (s < seqs) {
-        const int2 r = pool_range(p, seq0 + s, done);
-        // items lie at multiples of `together` blocks
+        const int2 r = pool_range<(kR > 0)>(p, seq0 + s, done);
+        // items lie at multiples of kTogether blocks
         if (r.y > r.x)
-          count[i] = static_cast<uint32_t>((r.y + p.together - 1) / p.together - r.x / p.together) * p.g.H_kv;
+          count[i] = static_cast<uint32_t>((r.y + kTogether - 1) / kTogether - r.x / kTogether) * p.g.H_kv;
         if (p.last_block && blockIdx.x == 0)
           for (int h = 0; h < p.g.H_kv; ++h)
             p.last_block[static_cast<int64_t>(seq0 + s) * p.g.H_kv + h] = done - 1;
@@ -492,19 +497,25 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
       int seq, h, b0, lo, hi;
       int64_t at;
     };
+    int known = -1;                                         // the sequence of `range`
+    int2 range = make_int2(0, 0);
+    uint32_t first = 0;                                     // its first item
     auto locate = [&](uint32_t it) -> Item {
       Item x{0, 0, 0, 0, 0, -1};
       if (it >= end) return x;
       while (it >= ends[s]) ++s;
+      if (s != known) {
+        int done;
+        range = pool_range<(kR > 0)>(p, seq0 + s, done);
+        first = s > 0 ? ends[s - 1] : 0;
+        known = s;
+      }
       x.seq = seq0 + s;
-      int done;
-      const int2 range = pool_range(p, x.seq, done);
-      const uint32_t local = it - (s > 0 ? ends[s - 1] : 0);
-      const uint32_t set = local / static_cast<uint32_t>(p.g.H_kv);
-      x.h = static_cast<int>(local - set * p.g.H_kv);
-      x.b0 = (range.x / p.together + static_cast<int>(set)) * p.together;
+      const uint32_t set = (it - first) / static_cast<uint32_t>(p.g.H_kv);
+      x.h = static_cast<int>(it - first - set * p.g.H_kv);
+      x.b0 = (range.x / kTogether + static_cast<int>(set)) * kTogether;
       x.lo = max(x.b0, range.x);
-      x.hi = min(x.b0 + p.together, range.y);
+      x.hi = min(x.b0 + kTogether, range.y);
       if constexpr (kR > 0) x.at = paged_slot(p.g, x.seq, x.b0 * p.block_size + part_of * kPoolRun);
       return x;
     };
@@ -579,24 +590,27 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
       }
       if (kR == 16 || kR == 0) {
         if (p.share > 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(&part[grp][8 * l + 2 * i]) = acc[i];
+          float4 (&at)[kPoolGroups][2][kPoolLanes] = part[turn & 1];
+          ++turn;
+          at[grp][0][l] = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
+          at[grp][1][l] = make_float4(acc[2].x, acc[2].y, acc[3].x, acc[3].y);
           __syncthreads();
+          if (!warp_joins) continue;
           if (part_of == 0)
-            for (int u = 1; u < p.share; ++u)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 o = *reinterpret_cast<const float2 *>(&part[grp + u][8 * l + 2 * i]);
-                acc[i].x += o.x;
-                acc[i].y += o.y;
-              }
-          __syncthreads();
+            for (int u = 1; u < p.share; ++u) {
+              const float4 a = at[grp + u][0][l], b = at[grp + u][1][l];
+              acc[0] = fadd2(acc[0], make_float2(a.x, a.y));
+              acc[1] = fadd2(acc[1], make_float2(a.z, a.w));
+              acc[2] = fadd2(acc[2], make_float2(b.x, b.y));
+              acc[3] = fadd2(acc[3], make_float2(b.z, b.w));
+            }
         }
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[2 * i] = __fdiv_rn(acc[i].x, size);
-          x[2 * i + 1] = __fdiv_rn(acc[i].y, size);
+          // a power of two's reciprocal gives the same quotient
+          x[2 * i] = kR > 0 ? acc[i].x * inv : __fdiv_rn(acc[i].x, size);
+          x[2 * i + 1] = kR > 0 ? acc[i].y * inv : __fdiv_rn(acc[i].y, size);
         }
         pool_store<kFp8>(x, p, cur.seq, cur.h, cur.b0, l, cur.hi > cur.lo && part_of == 0);
       }
