@@ -24,7 +24,8 @@
  * whose kept slots all have the logit -infinity. What masked slots hold, NaN
  * and infinities among it, has no effect; a NaN that is kept gives NaN. A weight
  * e^{l_s} takes part as a bf16 number relative to its row's largest (one below
- * 2^-126 of that may count as 0); sums are fp32.
+ * 2^-126 of that may count as 0); sums are fp32, of weights up to 2^8 times the
+ * final largest one: values of 2^100 and more may make them overflow.
  *
  * Where the operation is defined (page titles and sections):
  *  - NeMo AutoModel optimized_kernels, sparse_attention_torch and

@@ -418,3 +418,177 @@ def test_the_indexer_reads_appended_fp8_pages(dsa):
         exact = (exact * w[t].cpu().double().numpy()[:, None]).sum(axis=0)
         assert np.abs(ref - exact).max() <= 0.2 * np.abs(exact).max()       # quantisation alone
         assert set(top[t].cpu().tolist()) == set(np.argsort(-got, kind="stable")[:k_top].tolist())
+
+
+# ---- many items, many sequences, far offsets, one graph ------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bs", [3, 4])
+def test_pool_more_sequences_than_are_counted_at_once(dsa, bs, fp8):
+    """2,500 sequences of up to 32 slots."""
+    rng = np.random.default_rng(34)
+    c = Cache(rng, 2500, 2, 16, 1, fp8, values=False)
+    pos = rng.integers(-1, 32, 2500)
+    assert run_pool(dsa, c, bs, 32 // bs, np.maximum(0, pos - rng.integers(0, 9, 2500)), pos) > 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bs", [64, 100, 512])
+def test_pool_many_turns_a_block_of_threads(dsa, bs, fp8):
+    """More shared items than the GPU takes at once, twice to the same bits."""
+    rng = np.random.default_rng(35)
+    n, pages, ps, Hkv = 2, 1024, 128, 2
+    g = torch.Generator(device="cuda").manual_seed(35)
+    x = torch.randn((n * pages, ps, Hkv, D), generator=g, device="cuda")
+    table = torch.from_numpy(rng.permutation(n * pages).astype(np.int32).reshape(n, pages)).cuda()
+    if fp8:
+        data = (x * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+        scale = torch.randint(119, 122, data.shape[:-1] + (D // 32,), generator=g, device="cuda", dtype=torch.uint8)
+        rows = data.double() * torch.exp2(scale.double() - 127).repeat_interleave(32, dim=-1)
+    else:
+        data, scale = x.bfloat16(), None
+        rows = data.double()
+    cache = dsa.make_paged_cache(ps, pages, n * pages, table, num_seqs=n, H_kv=Hkv,
+                                 dtype=dsa.DSA_KV_FP8_E4M3_E8M0_B32 if fp8 else dsa.DSA_KV_BF16)
+    S_pool = pages * ps // bs
+    last = [pages * ps - 1, 100001]
+    desc = dsa.make_block_pool_desc(cache, bs, S_pool)
+    got = []
+    for _ in range(2):
+        pooled = torch.zeros((n, Hkv, S_pool, D), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+        ps_ = torch.zeros((n, Hkv, S_pool, D // 32), dtype=torch.uint8, device="cuda") if fp8 else None
+        dsa.dsa_block_pool(desc, data, scale, None, dev_i32(last), pooled, ps_, None,
+                           torch.cuda.current_stream().cuda_stream)
+        got.append((pooled, ps_))
+    assert torch.equal(got[0][0], got[1][0]) and (not fp8 or torch.equal(got[0][1], got[1][1]))
+    for i, p in enumerate(last):
+        done = (p + 1) // bs
+        mine = rows[table[i].long()].flatten(0, 1)[:done * bs].unflatten(0, (done, bs))
+        ref = mine.mean(dim=1).transpose(0, 1).cpu().numpy()
+        slack = np.full(ref.shape, (bs + 1) * 2.0 ** -24 * float(mine.abs().max()))
+        if fp8:
+            check_mx_rows(got[0][0][i, :, :done].cpu().numpy(), got[0][1][i, :, :done].cpu().numpy(), ref, slack)
+        else:
+            check_rows(got[0][0][i, :, :done].double().cpu().numpy(), ref, slack)
+        assert not got[0][0][i, :, done:].any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_and_pool_past_32_bit_offsets(dsa, fp8):
+    """Pages 2^31 elements apart: keys appended there, and their blocks pooled."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 20 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    rng = np.random.default_rng(36)
+    ps, far, L = 16, 2 ** 31, 45
+    size = 2 * far + ps * D
+    kp = torch.zeros(size, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    ks = torch.zeros(size // 32, dtype=torch.uint8, device="cuda") if fp8 else None
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    cache = dsa.make_paged_cache(ps, 3, 3, table, num_seqs=1, page_stride=far,
+                                 dtype=dsa.DSA_KV_FP8_E4M3_E8M0_B32 if fp8 else dsa.DSA_KV_BF16)
+    k = bf16_bits(rng.standard_normal((L, 1, D)))
+    stream = torch.cuda.current_stream().cuda_stream
+    dsa.dsa_cache_append(dsa.make_append_desc(cache, L, 0, 0), None, k.cuda(), None, None, None,
+                         dev_i32(np.arange(L)), dev_i32(np.zeros(L)), None, None, kp, ks, None, None, stream)
+    at = [([2, 0, 1][p // ps]) * far + p % ps * D for p in range(L)]
+    ref = k[:, 0].double().numpy()
+    data = torch.stack([kp[o:o + D] for o in at]).cpu()
+    if fp8:
+        scale = torch.stack([ks[o // 32:o // 32 + 4] for o in at]).cpu()
+        check_mx_rows(data.numpy(), scale.numpy(), ref, np.zeros_like(ref))
+        rows = decode_mx(data, scale)
+    else:
+        assert torch.equal(data, k[:, 0])
+        rows = ref
+    pooled = torch.zeros((11, D), dtype=kp.dtype, device="cuda")
+    pscale = torch.zeros((11, D // 32), dtype=torch.uint8, device="cuda") if fp8 else None
+    dsa.dsa_block_pool(dsa.make_block_pool_desc(cache, 4, 11), kp, ks, None, dev_i32([L - 1]), pooled, pscale,
+                       None, stream)
+    mean = rows[:44].reshape(11, 4, D).mean(axis=1)
+    slack = np.full(mean.shape, 5 * 2.0 ** -24 * np.abs(rows).max())
+    if fp8:
+        check_mx_rows(pooled.cpu().numpy(), pscale.cpu().numpy(), mean, slack)
+    else:
+        check_rows(pooled.double().cpu().numpy(), mean, slack)
+
+
+def test_a_whole_step_in_one_graph(dsa):
+    """Append, pooling, the indexer, attention over its blocks and over all
+    slots captured once, replayed for the next steps' positions, queries and
+    keys: each attention against the oracle on the rows then in the cache."""
+    rng = np.random.default_rng(43)
+    B, Hkv, G, bs, n, ps = 4, 2, 8, 16, 4, 32
+    H, S_pool = Hkv * G, 256 // bs
+    c = Cache(rng, B, 8, ps, Hkv)
+    dev, table = c.to("cuda")
+    for name in dev:
+        c.pools[name] = dev[name]
+    q, k, v = (torch.zeros((B, h, D), dtype=torch.bfloat16, device="cuda") for h in (H, Hkv, Hkv))
+    qr = torch.zeros_like(q)
+    cos, sin = torch.zeros((B, 32), device="cuda"), torch.zeros((B, 32), device="cuda")
+    pos, start = dev_i32([0] * B), dev_i32([0] * B)
+    pooled = torch.zeros((B, Hkv, S_pool, D), dtype=torch.bfloat16, device="cuda")
+    last = torch.zeros((B, Hkv), dtype=torch.int32, device="cuda")
+    w = torch.full((B * Hkv, G), 1.0 / G, device="cuda")
+    scores = torch.zeros((B * Hkv, S_pool), device="cuda")
+    top = torch.full((B, Hkv, n), -1, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    lses = [torch.zeros((B, H), device="cuda") for _ in range(2)]
+    cache = c.desc(dsa, table)
+    ad = dsa.make_append_desc(cache, B, H, 64)
+    pd = dsa.make_block_pool_desc(cache, bs, S_pool)
+    idesc = dsa.make_desc(B * Hkv, G, n, S=S_pool, k_seq_stride=S_pool * D)
+    iws = torch.zeros(dsa.dsa_indexer_workspace_size(idesc), dtype=torch.uint8, device="cuda")
+    bd = dsa.make_paged_attention_desc(cache, B, H, D ** -0.5, window=bs, block_size=bs, num_blocks=n,
+                                       block_heads=Hkv)
+    dd = dsa.make_paged_attention_desc(cache, B, H, D ** -0.5)
+    ws_bytes = max(dsa.dsa_paged_attention_workspace_size(x) for x in (bd, dd))
+    ws = torch.zeros(ws_bytes, dtype=torch.uint8, device="cuda")
+
+    def step():
+        s = torch.cuda.current_stream().cuda_stream
+        dsa.dsa_cache_append(ad, q, k, v, cos, sin, pos, None, qr, None, *dev["k"], *dev["v"], s)
+        dsa.dsa_block_pool(pd, *dev["k"], start, pos, pooled, None, last, s)
+        dsa.dsa_indexer_forward(idesc, qr, None, w, pooled, None, last, scores, top, iws, iws.numel(), s)
+        dsa.dsa_block_attention_forward(bd, qr, *dev["k"], *dev["v"], None, pos, None, top, outs[0], lses[0],
+                                        ws, ws_bytes, s)
+        dsa.dsa_paged_attention_forward(dd, qr, *dev["k"], *dev["v"], None, pos, None, outs[1], lses[1],
+                                        ws, ws_bytes, s)
+
+    def fill(at):
+        for x in (q, k, v):
+            x.copy_(bf16_bits(rng.standard_normal(tuple(x.shape))))
+        ang = at[:, None] * 10000.0 ** (-np.arange(32) / 32)
+        cos.copy_(torch.from_numpy(np.cos(ang).astype(np.float32)))
+        sin.copy_(torch.from_numpy(np.sin(ang).astype(np.float32)))
+        pos.copy_(dev_i32(at))
+
+    at = np.array([200, 63, 10, 127])
+    fill(at)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        start.copy_(dev_i32(at + 1))
+        at = at + 1
+        fill(at)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dsa.dsa_indexer_get_error(ws) == dsa.DSA_OK and dsa.dsa_indexer_get_error(iws) == dsa.DSA_OK
+        kr, vr, qn = c.rows("k"), c.rows("v"), qr.double().cpu().numpy()
+        for i in range(B):
+            assert torch.equal(torch.from_numpy(vr[c.table[i, at[i] // ps], at[i] % ps]), v[i].double().cpu())
+        done = (at + 1) // bs
+        assert np.array_equal(last.cpu().numpy(), np.repeat(done[:, None] - 1, Hkv, axis=1))
+        lists = top.cpu().numpy()
+        for i in range(B):
+            for g in range(Hkv):
+                mine = [b for b in lists[i, g] if b >= 0]
+                assert len(set(mine)) == len(mine) == min(n, done[i]) and all(b < done[i] for b in mine)
+        check_attention(outs[0], lses[0], orc.attention(qn, kr, vr, c.table, at, None, D ** -0.5, window=bs,
+                                                        blocks=lists, block_size=bs))
+        check_attention(outs[1], lses[1], orc.attention(qn, kr, vr, c.table, at, None, D ** -0.5))
