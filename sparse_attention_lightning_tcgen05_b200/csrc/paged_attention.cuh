@@ -142,10 +142,11 @@ struct PaSmem {
 // ends. A consumer warp takes every kWarps-th step with a running maximum, sum
 // and O (16 heads x 128 in registers) of its own, and (bf16) has the next step's
 // logits multiplied while it works on the present one's softmax. At an item's
-// end the warps add up from one to the next (a different first one each time,
-// so that none waits long); the last one writes. Items that lie in one CTA are
-// finished here; of the others each CTA leaves a partial result for the join
-// kernel.
+// end the warps add up from the first to the next, and the last one writes: always
+// in this order, so that from the second item on a warp ends when its turn comes (a
+// different first one each time, with a fence at every hand-over: 243 us where this
+// takes 234, below). Items that lie in one CTA are finished here; of the others each
+// CTA leaves a partial result for the join kernel.
 //
 // With up to 16 heads on a key-value head the products cost 8 flops a byte of
 // the cache at most, which mma.sync sustains beside HBM's rate; its fragments
@@ -153,11 +154,12 @@ struct PaSmem {
 // 128 rows on 16 heads and take a trip through TMEM a tile. Two CTAs an SM with
 // 192 KB (bf16) of stages between them cover HBM's latency. Measured on a B200:
 // 16 contexts of 2,048 to 32,768 slots, 8 key heads, bf16: 171 to 175 us, 6.7 TB/s
-// (HBM); 64 contexts of 1,024 to 32,768, 4 key heads, fp8: 228 to 241 us, 4.9 TB/s,
-// bound by the chain from a stage's bytes to fragments (about 700 instructions a
-// step of 32 slots; the loads alone take 181 us). One context of 1,000 slots: 12
+// (HBM); 64 contexts of 1,024 to 32,768, 4 key heads, fp8: 228 to 250 us, 4.9 to 4.6
+// TB/s, bound by the chain from a stage's bytes to fragments (about 700 instructions
+// a step of 32 slots; the loads alone take 181 us). One context of 1,000 slots: 12
 // us, a chain of launches, prologue, loads, hand-over and join. 1,024 tokens that
-// each list 16 blocks of 64: 245 to 250 us, the gathering of 2.3 GB out of L2.
+// each list 16 blocks of 64 and the last 64 slots: 234 us, of them 9.1 a block (2 GB
+// through the L2 in all, 13.9 TB/s), 15 fixed and 25 for the items' ends.
 template <bool kFp8, bool kList>
 __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -488,7 +490,11 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     // logit may pass it before O is rescaled (four lanes share a row's)
     float m[2] = {neg_inf, neg_inf}, mb[2] = {0.f, 0.f}, lazy[2] = {neg_inf, neg_inf};
     float sum[2] = {0.f, 0.f};
-    constexpr bool kAhead = !kFp8;                            // fp8: no registers for it
+    // The next step's logits ahead: not for fp8 (no registers), and not for listed
+    // blocks, which L2 feeds: holding two stages at once then costs more loads in
+    // flight than it hides (1,024 tokens, 16 blocks of 64 each: 243 us with, 210
+    // without; a batch over all its slots, which HBM feeds: 173 and 181).
+    constexpr bool kAhead = !kFp8 && !kList;
     float s[kJ][4], s_next[kAhead ? kJ : 1][4];
     uint32_t mask = 0, mask_next = 0;
     const int step0 = static_cast<int>((warp + kWarps - base_g % kWarps) % kWarps);
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     }
     base_g += it.steps;
 
-    // ---- add the warps' results up, warp n % kWarps first ----
+    // ---- add the warps' results up, from warp 0 to the last ----
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
@@ -628,42 +634,41 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
       // number, so that the sum is not taken for an empty one
       if (m[i] == neg_inf && sum[i] != 0.f) m[i] = 0.f;
     }
-    const int turn = static_cast<int>((warp + kWarps - n % kWarps) % kWarps);
     // the last item's sum is taken over (every warp waits: a wait below must
     // not meet the phase before)
     if (!pa_wait(hand_empty, (n & 1u) ^ 1u, ctl, 64)) return;
-    float *const hand = reinterpret_cast<float *>(smem + Smem::off_hand) + lane;
-    if (turn > 0) {
-      if (!pa_wait(hand_full + turn - 1, n & 1u, ctl, 65)) return;
+    float4 *const hand = reinterpret_cast<float4 *>(smem + Smem::off_hand) + lane;
+    if (warp > 0) {
+      if (!pa_wait(hand_full + warp - 1, n & 1u, ctl, 65)) return;
+      const float4 got = hand[0];
       float a[2], b[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float mo = hand[32 * i], M = fmaxf(m[i], mo);
+        const float mo = i ? got.y : got.x, M = fmaxf(m[i], mo);
         a[i] = m[i] == neg_inf ? 0.f : ex2_approx(m[i] - M);
         b[i] = mo == neg_inf ? 0.f : ex2_approx(mo - M);
-        sum[i] = a[i] * sum[i] + b[i] * hand[32 * (2 + i)];
+        sum[i] = a[i] * sum[i] + b[i] * (i ? got.w : got.z);
         m[i] = M;
       }
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[k][j] = fmaf(b[j >> 1], hand[32 * (4 + 4 * k + j)], a[j >> 1] * o[k][j]);
-    }
-    if (turn < kWarps - 1) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hand[32 * i] = m[i];
-        hand[32 * (2 + i)] = sum[i];
+      for (int k = 0; k < 16; ++k) {
+        const float4 x = hand[32 * (1 + k)];
+        o[k][0] = fmaf(b[0], x.x, a[0] * o[k][0]);
+        o[k][1] = fmaf(b[0], x.y, a[0] * o[k][1]);
+        o[k][2] = fmaf(b[1], x.z, a[1] * o[k][2]);
+        o[k][3] = fmaf(b[1], x.w, a[1] * o[k][3]);
       }
+    }
+    if (warp < kWarps - 1) {
+      hand[0] = make_float4(m[0], m[1], sum[0], sum[1]);
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hand[32 * (4 + 4 * k + j)] = o[k][j];
-      pa_release(hand_full + turn, lane);
+      for (int k = 0; k < 16; ++k) hand[32 * (1 + k)] = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+      __syncwarp();                                           // (read by a warp, not by TMA: no fence)
+      if (lane == 0) mbar_arrive(hand_full + warp);
       continue;
     }
-    pa_release(hand_empty, lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(hand_empty);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + 8 * i;

@@ -168,7 +168,7 @@ constexpr int kAppendLanes = kFp8 ? 8 : 16;
 // sines it reads once; four rows' loads are in flight a lane. Products and sums
 // of the rotation are rounded one by one (no fma), so that the result is the
 // formula's in fp32. Measured on a B200: 16 tokens (64 query heads, 8 key heads)
-// 2.5 us, a launch; 8,192 tokens bf16 64 us, 5.3 TB/s (copying reaches 6.6);
+// 2.4 us, a launch; 8,192 tokens bf16 65 us, 5.2 TB/s (copying reaches 6.6);
 // 12,345 tokens' 64 query heads and one key head to fp8 71 us, 4.4 TB/s, bound by
 // instructions (one group of 16 features a lane costs about 60).
 template <bool kQFp8, bool kKvFp8, bool kHalves>
@@ -236,6 +236,10 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
             s[u][i] = sr[i];
           }
       }
+      if (kHalves && f < p.half) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i) s[u][i] = -s[u][i];
+      }
     }
   }
 #pragma unroll
@@ -261,13 +265,16 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
         o.z = __shfl_sync(0xffffffffu, give.z, from, kLanes);
         o.w = __shfl_sync(0xffffffffu, give.w, from, kLanes);
         if (turn && r < v0) {
+          // (the low half's sines were negated: a cos + b (-sin) rounds as a cos - b sin)
           float y[8];
           unpack8(o, y);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float a = x[8 * u + j];
-            x[8 * u + j] = low ? __fsub_rn(__fmul_rn(a, c[u][j]), __fmul_rn(y[j], s[u][j]))
-                               : __fadd_rn(__fmul_rn(y[j], s[u][j]), __fmul_rn(a, c[u][j]));
+          for (int j = 0; j < 8; j += 2) {
+            float &a = x[8 * u + j], &b = x[8 * u + j + 1];
+            const float2 z = fadd2(fmul2(make_float2(a, b), make_float2(c[u][j], c[u][j + 1])),
+                                   fmul2(make_float2(y[j], y[j + 1]), make_float2(s[u][j], s[u][j + 1])));
+            a = z.x;
+            b = z.y;
           }
         }
       }
@@ -424,7 +431,8 @@ __device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &
 // that the result does not depend on timing). kR = 0: any block size, each row
 // looked up by itself, four in flight. Measured on a B200: a step of 64 sequences
 // 5.5 us (the chain start, positions, table, row); 240,000 bf16 keys by fours 12.2
-// us, 6.5 TB/s; 1.1 million fp8 rows by 64s 44 us, 3.2 TB/s, bound by instructions
+// us on resident rows and 17 on rows not in L2, 4.7 TB/s; 1.1 million fp8 rows by 64s
+// 37 us, 3.8 TB/s, bound by instructions
 // (four conversions to f16x2, eight to fp32 and four packed fmas a lane and row).
 template <bool kFp8, int kR>
 __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)

@@ -85,7 +85,7 @@ struct PaChain {
 struct PaRow {
   int seq, last;               // last = -1: nothing
   int lo;                      // first recent slot kept (dense: first slot kept)
-  int wbase;                   // lo rounded down to 32 slots
+  int wbase;                   // lo rounded down to 16 or (steps of 32 and more) 32 slots
   int steps;                   // of kStep slots, at least one
 };
 
@@ -99,7 +99,7 @@ __device__ __forceinline__ PaRow pa_row_of(const PagedAttnParams &p, int seq, in
   r.seq = seq;
   r.last = static_cast<int>(min(pos, cap - 1));
   r.lo = static_cast<int>(min(lo, static_cast<int64_t>(r.last) + 1));
-  r.wbase = r.lo & ~31;
+  r.wbase = r.lo & ~(kStep < 32 ? kStep - 1 : 31);
   r.steps = r.lo <= r.last ? (r.last + kStep - r.wbase) / kStep : 0;
   if (kList) r.steps += p.list_steps;
   r.steps = max(1, r.steps);
