@@ -111,3 +111,18 @@ def test_committed_profiles_name_their_sources_and_traffic():
         assert re.search(r"src_hash:\s*`[0-9a-f]{16}`", txt), n
         assert re.search(r"dram_bytes_per_launch:\s*`[0-9]+`", txt), n
         assert "--clock-control none" in txt, n
+
+
+def test_profiles_depend_on_the_timed_kernels_sources_alone(tmp_path, monkeypatch):
+    """Other sources beside them (host code, other operators) void no profile;
+    a change in one of them does."""
+    cs = tmp_path / "sparse_attention_lightning_tcgen05_b200" / "csrc"
+    cs.mkdir(parents=True)
+    for f in bench.KERNEL_SOURCES:
+        (cs / f).write_text(f)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    first = bench.source_hash()
+    (cs / "another.cuh").write_text("x")
+    assert bench.source_hash() == first
+    (cs / bench.KERNEL_SOURCES[0]).write_text("changed")
+    assert bench.source_hash() != first
