@@ -288,16 +288,22 @@ def dsa_indexer_prepare(desc, x, qr, wq_b, wk, weights_proj, k_norm_weight, k_no
         stream), "dsa_indexer_prepare")
 
 
+_current_device = None
+
+
 def _device_ptrs(where, *xs):
     """Device pointers of tensors, ints or None. A tensor that is not on the
     current CUDA device is refused: the library launches on that device."""
-    import torch
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = torch.cuda.current_device
     try:
-        current = torch.cuda.current_device()
+        current = _current_device()
     except (RuntimeError, AssertionError):        # no CUDA device, or no CUDA in torch
         current = -2
     # get_device() is -1 for host memory
-    return [x if x is None or isinstance(x, int) else
+    return [x if x is None or x.__class__ is int else
             x.data_ptr() if x.get_device() == current else _other_device(where, x, current)
             for x in xs]
 

@@ -117,7 +117,10 @@ struct PaSmem {
   // and 175, where the fewer stages cost more than the fifth warp brings.
   static constexpr int kWarps = kFp8 ? 5 : 4;
   static constexpr int kThreads = (kWarps + 1) * 32;                // and the producer
-  static constexpr int kLeast = 2 * kWarps;                         // steps worth a CTA
+  // Steps worth a CTA: one a consumer warp. One, two and three of them, us: one
+  // context of 4,000 slots, 8 key heads, bf16 10.9, 11.4, 13.6, fp8 11.7, 14.5, 15.0;
+  // 16 of 200 to 1,000 slots 15.0, 15.0, 15.0 and 17.3, 19.7, 22.2.
+  static constexpr int kLeast = kWarps;
   // three (bf16) or two a consumer warp; a stage is always the same warp's, so that no warp
   // waits for a phase before the last one of its barrier is over
   static constexpr int kStages = (kFp8 ? 2 : 3) * kWarps;
@@ -156,7 +159,7 @@ struct PaSmem {
 // 16 contexts of 2,048 to 32,768 slots, 8 key heads, bf16: 171 to 175 us, 6.7 TB/s
 // (HBM); 64 contexts of 1,024 to 32,768, 4 key heads, fp8: 228 to 250 us, 4.9 to 4.6
 // TB/s, bound by the chain from a stage's bytes to fragments (about 700 instructions
-// a step of 32 slots; the loads alone take 181 us). One context of 1,000 slots: 12
+// a step of 32 slots; the loads alone take 181 us). One context of 1,000 slots: 11.3
 // us, a chain of launches, prologue, loads, hand-over and join. 1,024 tokens that
 // each list 16 blocks of 64 and the last 64 slots: 234 us, of them 9.1 a block (2 GB
 // through the L2 in all, 13.9 TB/s), 15 fixed and 25 for the items' ends.
