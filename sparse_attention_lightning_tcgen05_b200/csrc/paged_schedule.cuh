@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "paged_cache.cuh"
+#include "paged_rows.h"
 #include "sm100_ptx.cuh"
 
 namespace dsa {
@@ -81,29 +82,9 @@ struct PaChain {
   }
 };
 
-// What a query token attends to: its sequence, last slot and recent slots.
-struct PaRow {
-  int seq, last;               // last = -1: nothing
-  int lo;                      // first recent slot kept (dense: first slot kept)
-  int wbase;                   // lo rounded down to 16 or (steps of 32 and more) 32 slots
-  int steps;                   // of kStep slots, at least one
-};
-
 template <bool kList, int kStep>
 __device__ __forceinline__ PaRow pa_row_of(const PagedAttnParams &p, int seq, int at) {
-  PaRow r;
-  const int64_t cap = p.g.capacity(), pos = at;
-  if (seq < 0 || seq >= p.g.num_seqs || pos < 0) return PaRow{0, -1, 0, 0, 1};
-  // window counts back from the token, which may stand past the table
-  const int64_t lo = (kList || p.window > 0) ? max(int64_t{0}, pos + 1 - p.window) : 0;
-  r.seq = seq;
-  r.last = static_cast<int>(min(pos, cap - 1));
-  r.lo = static_cast<int>(min(lo, static_cast<int64_t>(r.last) + 1));
-  r.wbase = r.lo & ~(kStep < 32 ? kStep - 1 : 31);
-  r.steps = r.lo <= r.last ? (r.last + kStep - r.wbase) / kStep : 0;
-  if (kList) r.steps += p.list_steps;
-  r.steps = max(1, r.steps);
-  return r;
+  return pa_row_at(p.g.capacity(), p.g.num_seqs, p.window, kList, p.list_steps, kStep, seq, at);
 }
 
 template <bool kList, int kStep>

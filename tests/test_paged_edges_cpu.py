@@ -1,0 +1,76 @@
+"""Edges of the paged operators that need no GPU: the kernels' row arithmetic
+at the ends of its range."""
+import pathlib
+import subprocess
+
+import pytest
+
+ROOT = pathlib.Path(__file__).resolve().parent.parent
+CSRC = ROOT / "sparse_attention_lightning_tcgen05_b200" / "csrc"
+
+_ROWS = r"""
+#include <cstdio>
+#include "paged_rows.h"
+int main() {
+  long long cap;
+  int num_seqs, window, list, list_steps, step, seq, at;
+  while (std::scanf("%lld %d %d %d %d %d %d %d", &cap, &num_seqs, &window, &list, &list_steps, &step,
+                    &seq, &at) == 8) {
+    const dsa::PaRow r = dsa::pa_row_at(cap, num_seqs, window, list != 0, list_steps, step, seq, at);
+    std::printf("%d %d %d %d %d\n", r.seq, r.last, r.lo, r.wbase, r.steps);
+  }
+  return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def rows_of():
+    out = ROOT / "_build" / "paged_rows"
+    out.mkdir(parents=True, exist_ok=True)
+    (out / "rows.cpp").write_text(_ROWS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-I", str(CSRC), str(out / "rows.cpp"), "-o",
+                    str(out / "rows")], check=True)
+
+    def run(cases):
+        text = "\n".join(" ".join(str(int(x)) for x in c) for c in cases)
+        got = subprocess.run([str(out / "rows")], input=text, capture_output=True, text=True, check=True).stdout
+        return [tuple(int(x) for x in line.split()) for line in got.splitlines()]
+    return run
+
+
+def expected_row(cap, num_seqs, window, is_list, list_steps, step, seq, at):
+    """The kept slots [lo, last] and the steps from wbase on, in whole numbers."""
+    if not 0 <= seq < num_seqs or at < 0:
+        return 0, -1, 0, 0, 1
+    last = min(at, cap - 1)
+    lo = min(max(0, at + 1 - window) if is_list or window > 0 else 0, last + 1)
+    unit = min(step, 32)
+    wbase = lo // unit * unit
+    steps = -(-(last + 1 - wbase) // step) if lo <= last else 0
+    return seq, last, lo, wbase, max(1, steps + (list_steps if is_list else 0))
+
+
+def test_rows_at_the_ends_of_the_range(rows_of):
+    """Sequences of up to 2^31 - 16 slots, the most that is accepted: the steps of
+    16, 32 and 128 slots to the last of them, with and without a window or a
+    list; and every small row."""
+    cases = []
+    for cap in (2 ** 31 - 16, 2 ** 31 - 32, 2 ** 31 - 64, 2 ** 31 - 128, 2 ** 31 - 65536):
+        for step in (16, 32, 128):
+            for window in (0, 1, 17, 128, 2 ** 31 - 1):
+                for is_list, list_steps in ((0, 0), (1, 5)):
+                    for at in (cap - 200, cap - 128, cap - 127, cap - 33, cap - 2, cap - 1, cap, 2 ** 31 - 1):
+                        if at < 2 ** 31:
+                            cases.append((cap, 1, window, is_list, list_steps, step, 0, at))
+    for cap in (16, 48):
+        for step in (16, 32, 128):
+            for window in (0, 1, 16, 20, 100):
+                for is_list in (0, 1):
+                    for seq in (-1, 0, 1, 2):
+                        for at in range(-2, 60):
+                            cases.append((cap, 2, window, is_list, 3, step, seq, at))
+    got = rows_of(cases)
+    assert len(got) == len(cases)
+    for c, row in zip(cases, got):
+        assert row == expected_row(*c), (c, row, expected_row(*c))
