@@ -7,12 +7,13 @@
 //   lse = ln sum_s e^{l_s}.
 // One pass over the slots with a running maximum m and sum, in log2 units:
 // p_s = 2^(x_s - m), x = l * log2(e); the accumulated O and the sum are
-// rescaled only when the maximum grows by more than 2^8 (p stays <= 256 and
-// the final division removes the common factor, so the result is the same).
+// rescaled only when the maximum grows by more than 8 (p stays <= 2^8 and the
+// final division removes the common factor, so the result is the same).
 // P is rounded to bf16 for its product with V, as V is: an error of half a
 // step (2^-9 on average) of each weight, which averages out over the slots.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -374,7 +375,12 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
 
     // ---- the query heads as matrix fragments ----
     uint32_t qf[8][4];
-    float xs[2] = {p.scale_log2, p.scale_log2};               // logit scale of rows r0, r0 + 8
+    // logit scale of rows r0, r0 + 8: a negative one's sign goes to the query, so
+    // that the largest product is the largest logit; 0 counts as the least normal
+    // number, so that a masked logit stays -infinity
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float scale = fabsf(p.scale_log2);
+    float xs[2] = {fmaxf(scale, FLT_MIN), fmaxf(scale, FLT_MIN)};
     {
       const uint8_t *const sq = smem + Smem::off_q;
       if constexpr (!kFp8) {
@@ -383,6 +389,8 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
           // matrices: rows 0-7, 8-15 of features 16kk .. + 7, then of + 8 .. + 15
           const int r = lane & 15, c = (2 * kk + (lane >> 4)) & 7;
           ldsm4(qf[kk], smem_u32(sq) + (kk >> 2) * (kPaRows * 128) + r * 128 + ((c ^ (r & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[kk][i] ^= flip;
         }
       } else {
         // features 16kk + 4 quad .. + 3: the order the fp8 keys' bytes come in
@@ -393,8 +401,8 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
             const int r = r0 + 8 * i, c = (2 * kk + (quad >> 1)) & 7;
             const uint2 w = *reinterpret_cast<const uint2 *>(
                 sq + (kk >> 2) * (kPaRows * 128) + r * 128 + ((c ^ (r & 7)) << 4) + 8 * (quad & 1));
-            qf[kk][i] = w.x;
-            qf[kk][2 + i] = w.y;
+            qf[kk][i] = w.x ^ flip;
+            qf[kk][2 + i] = w.y ^ flip;
           }
         // e4m3 keys are exact in f16, and so are the query's bf16 values once
         // its largest is brought to 2^13 .. 2^14: f16's 11 bits cover bf16's 8
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
           // inf and NaN stay as they are; 2^shift must be a normal number
           const int shift = top >= 0x7f80u || top == 0 ? 0 : max(-126, min(126, 13 - e));
           const float up = __int_as_float((shift + 127) << 23);
-          xs[i] = p.scale_log2 * __int_as_float((127 - shift) << 23);
+          xs[i] = fmaxf(scale * __int_as_float((127 - shift) << 23), FLT_MIN);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
@@ -489,9 +497,12 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     for (int i = 0; i < 16; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    // the running maximum, 0 instead of it while there is none, and how far a
-    // logit may pass it before O is rescaled (four lanes share a row's)
-    float m[2] = {neg_inf, neg_inf}, mb[2] = {0.f, 0.f}, lazy[2] = {neg_inf, neg_inf};
+    // The running maximum (of unscaled logits until the item's end), 0 instead of
+    // it while there is none, and the logit past which O is rescaled (four lanes
+    // share a row's). The maximum is taken off before the scaling: the largest
+    // weight is then exactly 1 however large the logits are, where an fma of scaled
+    // ones leaves what the maximum's own rounding dropped, hundreds at 2^33.
+    float m[2] = {neg_inf, neg_inf}, mb[2] = {0.f, 0.f}, limit[2] = {neg_inf, neg_inf};
     float sum[2] = {0.f, 0.f};
     // The next step's logits ahead: not for fp8 (no registers), and not for listed
     // blocks, which L2 feeds: holding two stages at once then costs more loads in
@@ -512,10 +523,6 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
       uint8_t *const stage = smem + st * Smem::kStageBytes;
       const uint32_t vs = smem_u32(stage) + Smem::off_v;
       // ---- softmax: rows r0 and r0 + 8, slots 8j + 2 quad + {0, 1} ----
-#pragma unroll
-      for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[j][i] = fmaf(s[j][i], xs[i >> 1], -mb[i >> 1]);
       if (mask != kAll) {
         // value rows of slots that are not kept: their weight is 0, and 0
         // times whatever is there has to be 0
@@ -537,36 +544,34 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
       for (int j = 0; j < kJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i >> 1] = fmaxf(mx[i >> 1], s[j][i]);
-      if (__any_sync(0xffffffffu, mx[0] > lazy[0] || mx[1] > lazy[1])) {
+      if (__any_sync(0xffffffffu, mx[0] > limit[0] || mx[1] > limit[1])) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-          const float mn = fmaxf(m[i], mx[i] + mb[i]);
+          const float mn = fmaxf(m[i], mx[i]);
           if (mn == neg_inf) continue;
-          const float a = m[i] == neg_inf ? 0.f : ex2_approx(m[i] - mn);
-          const float down = mb[i] - mn;
+          const float a = m[i] == neg_inf ? 0.f : ex2_approx((m[i] - mn) * xs[i]);
           m[i] = mb[i] = mn;
-          lazy[i] = kPaLazy;
+          limit[i] = __fadd_rd(mn, __fdividef(kPaLazy, xs[i]));
           sum[i] *= a;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             o[k][2 * i] *= a;
             o[k][2 * i + 1] *= a;
           }
-#pragma unroll
-          for (int j = 0; j < kJ; ++j) {
-            s[j][2 * i] += down;
-            s[j][2 * i + 1] += down;
-          }
         }
       }
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[j][i] = ex2_approx(s[j][i]);
-          sum[i >> 1] += s[j][i];
+        for (int i = 0; i < 2; ++i) {
+          const float2 x = fmul2(fadd2(make_float2(s[j][2 * i], s[j][2 * i + 1]), make_float2(-mb[i], -mb[i])),
+                                 make_float2(xs[i], xs[i]));
+          s[j][2 * i] = ex2_approx(x.x);
+          s[j][2 * i + 1] = ex2_approx(x.y);
+          sum[i] += s[j][2 * i];
+          sum[i] += s[j][2 * i + 1];
         }
       // ---- O += P V ----
       if constexpr (!kFp8) {
@@ -633,9 +638,10 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-      // no maximum although slots were kept, their logits being NaN: any
-      // number, so that the sum is not taken for an empty one
-      if (m[i] == neg_inf && sum[i] != 0.f) m[i] = 0.f;
+      // in log2 units from here on; no maximum although slots were kept, their
+      // logits being NaN: any number, so that the sum is not taken for an empty one
+      if (m[i] != neg_inf) m[i] *= xs[i];
+      else if (sum[i] != 0.f) m[i] = 0.f;
     }
     // the last item's sum is taken over (every warp waits: a wait below must
     // not meet the phase before)

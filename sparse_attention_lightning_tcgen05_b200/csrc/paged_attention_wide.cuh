@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
       const PaItem it = *info;
       if (it.row < 0) break;
       pa_release(q_empty, lane);
+      // (the maximum unscaled until the item's end, as in the other kernel)
       float m = neg_inf, mb = 0.f, lazy = neg_inf, sum = 0.f;
       bool first = true;
       for (int i = (stream ^ g) & 1; i < it.steps; i += 2) {
@@ -555,12 +556,12 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
           }
           ahead(0);                                           // for the second reading
           const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          // a logit of the row's largest, or -inf where nothing is kept
-          const float mx = top == neg_inf ? neg_inf : top * fabsf(p.scale_log2);
-          const bool grow = mine && mx - mb > lazy;
+          // the row's largest logit before its scaling (-inf: nothing is kept)
+          const float mx = down_scale ? -top : top;
+          const bool grow = mine && top != neg_inf && (mx - mb) * p.scale_log2 > lazy;
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mx : mb;                  // the row's new reference
-            const float a = !grow ? 1.f : m == neg_inf ? 0.f : ex2_approx(m - mn);
+            const float a = !grow ? 1.f : m == neg_inf ? 0.f : ex2_approx((m - mn) * p.scale_log2);
             if (!first) {
               // O holds the stream's earlier tiles: their P V ended before this
               // tile's S, which products issued in order
@@ -589,7 +590,12 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
             tmem_wait_ld32(x);
             if (q4 < 3) ahead(q4 + 1);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = fmaf(x[c], p.scale_log2, -mb);
+            for (int c = 0; c < 32; c += 2) {
+              const float2 y = fmul2(fadd2(make_float2(x[c], x[c + 1]), make_float2(-mb, -mb)),
+                                     make_float2(p.scale_log2, p.scale_log2));
+              x[c] = y.x;
+              x[c + 1] = y.y;
+            }
             if (!every) {
 #pragma unroll
               for (int c = 0; c < 32; ++c)
@@ -614,7 +620,9 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
         if (lane == 0) mbar_arrive(p_full + stream);
       }
       if (!ok) break;
-      if (m == neg_inf && sum != 0.f) m = 0.f;                // all kept logits NaN: not an empty row
+      // in log2 units from here on; all kept logits NaN: not an empty row
+      if (m != neg_inf) m *= p.scale_log2;
+      else if (sum != 0.f) m = 0.f;
       // ---- add the two streams up: this one writes half of the features ----
       // (once everyone has read the last item's maxima and sums)
       if (n > 0 && !pa_wait(o_free, (n - 1) & 1u, ctl, 83)) break;

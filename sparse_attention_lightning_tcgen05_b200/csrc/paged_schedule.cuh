@@ -17,7 +17,7 @@
 
 namespace dsa {
 
-constexpr float kPaLazy = 8.f;                     // log2 units: rescale when the maximum grows by more
+constexpr float kPaLazy = 8.f;                     // log2 units: rescale when a logit passes the maximum by more
 constexpr float kPaLog2e = 1.4426950408889634f;
 constexpr float kPaLn2 = 0.6931471805599453f;
 

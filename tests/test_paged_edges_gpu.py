@@ -54,3 +54,55 @@ def test_the_last_slots_of_the_longest_sequence(dsa, H, fp8, ps):
     ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, [small - 1], None, SCALE,
                         blocks=np.array([[[3, 1, -1]]]), block_size=ps, window=7)
     check_attention(out, lse, ref)
+
+
+@pytest.mark.parametrize("T", [1, 64])
+@pytest.mark.parametrize("top", [2.0 ** 12, 2.0 ** 24, 2.0 ** 28, 2.0 ** 31, 2.0 ** 33, 1e10, 1e30])
+@pytest.mark.parametrize("G,fp8", [(8, False), (8, True), (64, False), (64, True)])
+def test_large_finite_logits(dsa, G, fp8, top, T):
+    """Logits up to `top` that grow along the slots, the largest three times, for
+    every other head the smallest three times (a negative query). Keys and queries
+    have one feature, so that logits are exact products; neighbouring ones are a
+    sixteenth apart at least, hundreds of the largest logit's rounding steps, so
+    that only the three count, with the same weight: out is their values' mean,
+    off by its rounding (2^-8) and the fp32 sums' (2^-20 covers three terms and the
+    division), lse the largest logit + ln 3 by relative 2^-21 (a scale, a product,
+    a sum and the factor ln 2 in fp32, half a step each). One token, whose steps lie
+    in as many warps, or 64 equal ones, where a warp has several."""
+    rng = np.random.default_rng(62)
+    c = Cache(rng, 1, 16, 64, 1, fp8)
+    n = 1000
+    order = np.sort(rng.integers(0x31, 0x77, n)).astype(np.uint8)
+    order[:3], order[3:] = 0x30, np.maximum(order[3:], 0x31)
+    order[-3:], order[:-3] = 0x77, np.minimum(order[:-3], 0x76)
+    last, first = [400, 700, n - 1], [0, 333, 800]
+    for a, b in zip(last + first, [n - 1, n - 2, n - 3, 0, 1, 2]):
+        order[a], order[b] = order[b], order[a]
+    value = torch.from_numpy(order).view(torch.float8_e4m3fn).double().numpy()
+    last, first = np.flatnonzero(order == 0x77), np.flatnonzero(order == 0x30)
+    assert len(last) == len(first) == 3
+    page, slot = c.table[0][np.arange(n) // 64], np.arange(n) % 64
+    if fp8:
+        data, scale = c.pools["k"]
+        data.zero_()
+        scale.fill_(127)
+        data[c.at[page, slot, 0]] = torch.from_numpy(order)
+    else:
+        rows = np.zeros((c.num_pages, 64, 1, D))
+        rows[page, slot, 0, 0] = value
+        c.set_rows("k", rows)
+    q = torch.zeros((T, G, D), dtype=torch.bfloat16)
+    q[:, ::2, 0], q[:, 1::2, 0] = 1.0, -1.0
+    dev, table = c.to("cuda")
+    amp = float(np.float32(top / value.max()))
+    out, lse = attend(dsa, c, dev, table, q.cuda(), np.full(T, n - 1), amp, seq_ids=np.zeros(T))
+    v = c.rows("v")[page, slot, 0]
+    for h in range(G):
+        mine, sign = (first, -1.0) if h % 2 else (last, 1.0)
+        if h % 2 and amp * value.min() / 16 < 40:           # the smallest are not far enough apart
+            continue
+        ref, size = v[mine].mean(axis=0), np.abs(v[mine]).mean(axis=0)
+        got = out[:, h].double().cpu().numpy()
+        assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * size), h
+        x = sign * amp * value[mine[0]] + np.log(3.0)
+        assert np.all(np.abs(lse[:, h].double().cpu().numpy() - x) <= 2.0 ** -21 * abs(x)), h
