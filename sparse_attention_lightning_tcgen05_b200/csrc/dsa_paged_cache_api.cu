@@ -161,6 +161,7 @@ dsa_status_t dsa_cache_append(const dsa_append_desc_t *desc, const void *q, cons
   p.units = (p.rows + dsa::kAppendRows - 1) / dsa::kAppendRows;
   p.half = desc->rope_dim / 2;
   p.vec = p.half % 4 == 0 && aligned(cos, 16) && aligned(sin, 16);
+  p.minus_zero = -0.f;
   p.q_stride = desc->q_stride;
   p.k_stride = desc->k_stride;
   p.v_stride = desc->v_stride;

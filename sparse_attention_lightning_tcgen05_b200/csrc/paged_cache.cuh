@@ -100,7 +100,8 @@ __device__ __forceinline__ uint32_t largest_bits(const float (&x)[kN]) {
   return __float_as_uint(top) & 0x7fffffffu;
 }
 
-// Two products, each rounded to fp32.
+// Two products, each rounded to fp32; where they are summands, the compiler makes
+// an fma of product and sum all the same (rounded_products keeps them apart).
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
@@ -111,6 +112,12 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+
+// Two products, each rounded to fp32 whatever is done with them: minus_zero is
+// -0, which adds nothing to any product, but known at run time alone.
+__device__ __forceinline__ float2 rounded_products(float2 a, float2 b, float minus_zero) {
+  return ffma2(a, b, make_float2(minus_zero, minus_zero));
 }
 
 // Two sums, each rounded to fp32.
@@ -147,6 +154,7 @@ struct AppendParams {
   int units;                 // kAppendRows-row groups a token
   int half;                  // rope_dim / 2
   bool vec;                  // cos and sin rows can be read 16 bytes at a time
+  float minus_zero;          // -0 (rounded_products)
   int64_t q_stride, k_stride, v_stride;
   const uint16_t *q, *k, *v;
   const float *cos, *sin;
@@ -271,8 +279,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
             float &a = x[8 * u + j], &b = x[8 * u + j + 1];
-            const float2 z = fadd2(fmul2(make_float2(a, b), make_float2(c[u][j], c[u][j + 1])),
-                                   fmul2(make_float2(y[j], y[j + 1]), make_float2(s[u][j], s[u][j + 1])));
+            const float2 z = fadd2(
+                rounded_products(make_float2(a, b), make_float2(c[u][j], c[u][j + 1]), p.minus_zero),
+                rounded_products(make_float2(y[j], y[j + 1]), make_float2(s[u][j], s[u][j + 1]), p.minus_zero));
             a = z.x;
             b = z.y;
           }
@@ -284,8 +293,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Appe
         if (kF / 2 * l + j < p.half) {
           // (a cos, a sin) + (-b sin, b cos)
           const float a = x[2 * j], b = x[2 * j + 1], cj = c[j >> 2][j & 3], sj = s[j >> 2][j & 3];
-          const float2 y = fadd2(fmul2(make_float2(a, a), make_float2(cj, sj)),
-                                 fmul2(make_float2(b, b), make_float2(-sj, cj)));
+          const float2 y = fadd2(rounded_products(make_float2(a, a), make_float2(cj, sj), p.minus_zero),
+                                 rounded_products(make_float2(b, b), make_float2(-sj, cj), p.minus_zero));
           x[2 * j] = y.x;
           x[2 * j + 1] = y.y;
         }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import oracle.paged as orc
-from paged_util import D, Cache, attend, bf16_bits, check_attention, dev_i32
+from paged_util import D, Cache, attend, bf16_bits, check_attention, decode_mx, dev_i32
 
 pytestmark = pytest.mark.gpu
 SCALE = D ** -0.5
@@ -106,3 +106,58 @@ def test_large_finite_logits(dsa, G, fp8, top, T):
         assert np.all(np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * size), h
         x = sign * amp * value[mine[0]] + np.log(3.0)
         assert np.all(np.abs(lse[:, h].double().cpu().numpy() - x) <= 2.0 ** -21 * abs(x)), h
+
+
+def mx_rows(x):
+    """e4m3 bytes and e8m0 bytes of float32 rows (the format's rule, on the host)."""
+    e = orc.mx_exponents(x.astype(np.float64))
+    y = x.astype(np.float64) * np.repeat(2.0 ** -e.astype(np.float64), 32, axis=-1)       # exact
+    data = torch.from_numpy(y.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8)
+    return data.numpy(), (e + 127).astype(np.uint8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("rope_dim", [30, 64, 128])
+def test_append_rounds_every_product_and_the_sum(dsa, rope_dim, halves, fp8):
+    """The rotation is the stated fp32 formula to the last bit: two products, each
+    rounded, and their rounded sum. Half of the pairs cancel (equal features under
+    equal factors), where a product that is not rounded leaves a remainder."""
+    if halves and rope_dim % 16:
+        rope_dim = 48
+    rng = np.random.default_rng(63)
+    T, H, half = 300, 5, rope_dim // 2
+    c = Cache(rng, T, 1, 16, 2, fp8, values=False)
+    x = rng.standard_normal((T, H + 2, D))
+    cos, sin = rng.standard_normal((2, T, half)).astype(np.float32)
+    first = np.arange(half) if halves else 2 * np.arange(half)
+    second = first + (half if halves else 1)
+    same = rng.random((T, half)) < 0.5
+    sin = np.where(same, cos, sin)
+    x[:, :, second] = np.where(same[:, None], x[:, :, first], x[:, :, second])
+    x = bf16_bits(x)
+    a, b = x.float().numpy()[..., first], x.float().numpy()[..., second]
+    want = x.float().numpy().copy()
+    want[..., first] = a * cos[:, None] - b * sin[:, None]          # float32, each operation rounded
+    want[..., second] = a * sin[:, None] + b * cos[:, None]
+    dev, table = c.to("cuda")
+    kd, ks = dev["k"]
+    q_out = torch.zeros((T, H, D), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    q_scale = torch.zeros((T, H, D // 32), dtype=torch.uint8, device="cuda") if fp8 else None
+    desc = dsa.make_append_desc(c.desc(dsa, table), T, H, rope_dim, q_dtype=int(fp8),
+                                rope_style=dsa.DSA_ROPE_HALVES if halves else dsa.DSA_ROPE_INTERLEAVED)
+    pos = rng.integers(0, 16, T)
+    dsa.dsa_cache_append(desc, x[:, :H].contiguous().cuda(), x[:, H:].contiguous().cuda(), None,
+                         torch.from_numpy(cos).cuda(), torch.from_numpy(sin).cuda(), dev_i32(pos), None, q_out,
+                         q_scale, kd, ks, None, None, torch.cuda.current_stream().cuda_stream)
+    at = c.at[c.table[:, 0], pos]                                   # [T, 2]
+    rows = kd.cpu().view(torch.uint8 if fp8 else torch.bfloat16)[at[..., None] + torch.arange(D)]
+    if fp8:
+        scales = ks.cpu()[at[..., None] // 32 + torch.arange(D // 32)]
+        for got, got_s, ref in ((q_out.cpu(), q_scale.cpu(), want[:, :H]), (rows, scales, want[:, H:])):
+            data, e = mx_rows(ref)
+            assert np.array_equal(got_s.numpy(), e)
+            assert np.array_equal(decode_mx(got, got_s), decode_mx(torch.from_numpy(data), torch.from_numpy(e)))
+    else:
+        ref = torch.from_numpy(want).to(torch.bfloat16)
+        assert torch.equal(q_out.cpu(), ref[:, :H]) and torch.equal(rows, ref[:, H:])
