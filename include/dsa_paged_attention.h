@@ -22,7 +22,8 @@
  * token with no kept slot (a negative position, a sequence outside
  * [0, num_seqs), a list of -1) gets out = 0 and lse = -infinity, as does one
  * whose kept slots all have the logit -infinity. What masked slots hold, NaN
- * and infinities among it, has no effect; a NaN that is kept gives NaN. A weight
+ * and infinities among it, has no effect; a NaN that is kept gives NaN, and beside
+ * other slots so may an infinite value whose weight is 0. A weight
  * e^{l_s} takes part as a bf16 number relative to its row's largest (one below
  * 2^-126 of that may count as 0); sums are fp32, of weights up to 2^8 times the
  * final largest one: values of 2^100 and more may make them overflow.

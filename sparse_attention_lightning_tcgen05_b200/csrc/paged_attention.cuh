@@ -682,6 +682,12 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + 8 * i;
       if (r >= heads) continue;
+      if (m[i] == neg_inf) {
+        // nothing kept but logits of -infinity, whose weights of 0 make NaN of an
+        // infinite value
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k][2 * i] = o[k][2 * i + 1] = 0.f;
+      }
       if (it.slot < 0) {
         const int64_t row = static_cast<int64_t>(it.row) * p.H + h0 + r;
         float den = sum[i];

@@ -161,3 +161,29 @@ def test_append_rounds_every_product_and_the_sum(dsa, rope_dim, halves, fp8):
     else:
         ref = torch.from_numpy(want).to(torch.bfloat16)
         assert torch.equal(q_out.cpu(), ref[:, :H]) and torch.equal(rows, ref[:, H:])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("G", [8, 64])
+def test_rows_of_infinitely_small_logits_are_empty(dsa, G, bad):
+    """Every kept slot's logit is -infinity, its value infinite or NaN: out = 0 and
+    lse = -infinity, in one CTA and in many, beside rows that are as ever."""
+    rng = np.random.default_rng(64)
+    c = Cache(rng, 3, 80, 64, 1)
+    for name, x in (("k", -np.inf), ("v", bad)):
+        rows = c.rows(name)
+        for i, n in ((0, 5), (1, 5000)):
+            s = np.arange(n)
+            rows[c.table[i, s // 64], s % 64, 0, 3] = x
+        c.set_rows(name, rows)
+    dev, table = c.to("cuda")
+    q = queries(rng, 3, G)
+    q[:2, :, 3] = q[:2, :, 3].abs() + 1
+    pos = np.array([4, 4999, 100])
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE)
+    assert torch.all(out[:2] == 0) and torch.all(lse[:2] == float("-inf"))
+    ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, [-1, -1, 100], None, SCALE)
+    check_attention(out, lse, ref)
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE, blocks=np.array([[[0, -1]], [[3, 60]], [[-1, 0]]]),
+                      block_size=64)
+    assert torch.all(out[:2] == 0) and torch.all(lse[:2] == float("-inf")) and torch.isfinite(lse[2]).all()
