@@ -68,6 +68,9 @@ typedef struct {
                               the descriptor serves attention over all slots    */
   int32_t block_heads;     /* block attention: 1 (one list for every head) or
                               H_kv (one for each key-value head)                */
+  uint32_t flags;          /* 0, or DSA_FLAG_SELFTEST_STALL (dsa_indexer.h): a
+                              warp keeps back an arrival that others wait for, so
+                              that the wait limit runs out and is reported       */
   uint64_t wait_limit_ns;  /* device-side wait limit; 0 = the default, 4 s      */
 } dsa_paged_attention_desc_t;
 

@@ -97,7 +97,8 @@ class dsa_paged_attention_desc_t(ctypes.Structure):
     _fields_ = [("cache", dsa_paged_cache_t), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("sm_scale", ctypes.c_float), ("window", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
-                ("block_heads", ctypes.c_int32), ("wait_limit_ns", ctypes.c_uint64)]
+                ("block_heads", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("wait_limit_ns", ctypes.c_uint64)]
 
 
 class DsaError(RuntimeError):
@@ -363,11 +364,12 @@ def dsa_block_pool(desc, k_cache, k_scale, start, positions, pooled, pooled_scal
 
 
 def make_paged_attention_desc(cache, T, H, sm_scale, *, window=0, block_size=0, num_blocks=0,
-                              block_heads=1, wait_limit_ns=0):
+                              block_heads=1, flags=0, wait_limit_ns=0):
     """block_size and num_blocks: for dsa_block_attention_forward."""
     return dsa_paged_attention_desc_t(cache=cache, T=T, H=H, sm_scale=sm_scale, window=window,
                                       block_size=block_size, num_blocks=num_blocks,
-                                      block_heads=block_heads, wait_limit_ns=wait_limit_ns)
+                                      block_heads=block_heads, flags=flags,
+                                      wait_limit_ns=wait_limit_ns)
 
 
 def dsa_paged_attention_workspace_size(desc) -> int:

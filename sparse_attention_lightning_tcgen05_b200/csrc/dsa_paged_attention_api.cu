@@ -31,6 +31,7 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
   if (d->T < 1 || d->H < 1 || d->H % d->cache.H_kv != 0 || d->window < 0 ||
       !std::isfinite(d->sm_scale * dsa::kPaLog2e))
     return DSA_ERR_INVALID_ARG;
+  if (d->flags & ~DSA_FLAG_SELFTEST_STALL) return DSA_ERR_INVALID_ARG;
   if (d->H / d->cache.H_kv > 128) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->T) * d->H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   // a tensor map's strides are below 2^40 bytes
@@ -166,6 +167,7 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   p.chain = reinterpret_cast<int4 *>(p.part_ml + part_rows(plan));
   p.err = static_cast<unsigned int *>(workspace);
   p.err_info = p.err + 1;
+  p.selftest_stall = (d->flags & DSA_FLAG_SELFTEST_STALL) != 0;
   p.wait_limit_ns = d->wait_limit_ns ? d->wait_limit_ns : kPaWaitLimitNs;
   p.drain_limit_ns = kPaDrainLimitNs;
   CUtensorMap tq, tk, tv;

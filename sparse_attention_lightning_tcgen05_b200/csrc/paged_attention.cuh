@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
 #pragma unroll
       for (int k = 0; k < 16; ++k) hand[32 * (1 + k)] = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
       __syncwarp();                                           // (read by a warp, not by TMA: no fence)
-      if (lane == 0) mbar_arrive(hand_full + warp);
+      if (lane == 0 && !(p.selftest_stall && warp == 0)) mbar_arrive(hand_full + warp);
       continue;
     }
     __syncwarp();

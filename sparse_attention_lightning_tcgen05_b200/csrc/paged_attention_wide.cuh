@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(PwSmem<kFp8>::kThreads, 1)
       // (once everyone has read the last item's maxima and sums)
       if (n > 0 && !pa_wait(o_free, (n - 1) & 1u, ctl, 83)) break;
       ml[stream * kPwRows + r] = make_float2(m, sum);
-      pa_release(ml_full, lane);
+      if (!(p.selftest_stall && warp == 0)) pa_release(ml_full, lane);
       if (!pa_wait(ml_full, n & 1u, ctl, 81) || !pa_wait(item_done, n & 1u, ctl, 82)) break;
       tc_fence_after_sync();
       if (warp_rows) {

@@ -41,6 +41,7 @@ struct PagedAttnParams {
   int4 *chain;                 // items that several CTAs share (PaChain)
   bool chain_by_item;          // an entry an item, else one a CTA
   int ctas;                    // of the attention kernel
+  bool selftest_stall;         // warp 0's results never reach the others
   unsigned int *err, *err_info;
   uint64_t wait_limit_ns, drain_limit_ns;
 };

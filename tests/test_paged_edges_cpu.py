@@ -74,3 +74,24 @@ def test_rows_at_the_ends_of_the_range(rows_of):
     assert len(got) == len(cases)
     for c, row in zip(cases, got):
         assert row == expected_row(*c), (c, row, expected_row(*c))
+
+
+def test_attention_flags():
+    """The self-test flag is accepted, any other one refused; the field lies where
+    the descriptor had a gap, so that its size and its other offsets are as they were."""
+    import ctypes
+
+    import sparse_attention_lightning_tcgen05_b200 as dsa
+    cache = dsa.make_paged_cache(64, 16, 40, 1 << 20, num_seqs=2, H_kv=2)
+
+    def size(flags):
+        return dsa.dsa_paged_attention_workspace_size(
+            dsa.make_paged_attention_desc(cache, 3, 4, 0.1, flags=flags))
+    assert size(dsa.DSA_FLAG_SELFTEST_STALL) == size(0)
+    for flags in (1, 3, 4, 1 << 31):
+        with pytest.raises(dsa.DsaError) as e:
+            size(flags)
+        assert e.value.status == dsa.DSA_ERR_INVALID_ARG
+    t = dsa.dsa_paged_attention_desc_t
+    assert t.flags.offset == t.block_heads.offset + 4 and t.wait_limit_ns.offset == t.block_heads.offset + 8
+    assert ctypes.sizeof(t) == t.wait_limit_ns.offset + 8

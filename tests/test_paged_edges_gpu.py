@@ -187,3 +187,41 @@ def test_rows_of_infinitely_small_logits_are_empty(dsa, G, bad):
     out, lse = attend(dsa, c, dev, table, q.cuda(), pos, SCALE, blocks=np.array([[[0, -1]], [[3, 60]], [[-1, 0]]]),
                       block_size=64)
     assert torch.all(out[:2] == 0) and torch.all(lse[:2] == float("-inf")) and torch.isfinite(lse[2]).all()
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("T", [4, 400])
+@pytest.mark.parametrize("H,fp8", [(8, False), (8, True), (64, False), (64, True)])
+def test_a_stalled_call_reports_the_timeout(dsa, H, fp8, T, listed):
+    """A warp keeps an arrival back, others wait for it and give up after a
+    millisecond: the status is reported once, nothing past the call's rows is
+    written (whatever an earlier call left in the workspace), and the next call on
+    the same workspace is right. Few long items, which many CTAs share, and many
+    short ones."""
+    rng = np.random.default_rng(65)
+    c = Cache(rng, 4, 32, 64, 1, fp8)
+    dev, table = c.to("cuda")
+    q, seq = queries(rng, T, H), np.arange(T) % 4
+    pos = rng.integers(1000, 2048, T) if T == 4 else rng.integers(-1, 300, T)
+    blocks = rng.integers(-1, 32, (T, 1, 3)) if listed else None
+    more = dict(block_size=64, num_blocks=3, window=20) if listed else {}
+    desc = dsa.make_paged_attention_desc(c.desc(dsa, table), T, H, SCALE, wait_limit_ns=1_000_000,
+                                         flags=dsa.DSA_FLAG_SELFTEST_STALL, **more)
+    n = dsa.dsa_paged_attention_workspace_size(desc)
+    stream = torch.cuda.current_stream().cuda_stream
+    lists = [dev_i32(blocks)] if listed else []
+    call = dsa.dsa_block_attention_forward if listed else dsa.dsa_paged_attention_forward
+    qc, dpos, dseq = q.cuda(), dev_i32(pos), dev_i32(seq)
+    for fill in (0, 1, 0x70):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        out = torch.full((T + 60, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((T + 60, H), 7.0, device="cuda")
+        call(desc, qc, *dev["k"], *dev["v"], None, dpos, dseq, *lists, out, lse, ws, n, stream)
+        assert dsa.dsa_indexer_get_error(ws, stream) == dsa.DSA_ERR_TIMEOUT
+        assert dsa.dsa_indexer_get_error(ws, stream) == dsa.DSA_OK
+        assert torch.all(out[T:] == 7.0) and torch.all(lse[T:] == 7.0)
+        kw = dict(blocks=blocks, block_size=64, window=20) if listed else {}
+        got = attend(dsa, c, dev, table, qc, pos, SCALE, seq_ids=seq, workspace=ws, **kw)
+    ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, seq, SCALE, **kw)
+    check_attention(*got, ref)
