@@ -292,9 +292,10 @@ def dsa_indexer_prepare(desc, x, qr, wq_b, wk, weights_proj, k_norm_weight, k_no
 _current_device = None
 
 
-def _device_ptrs(where, *xs):
+def _device_ptrs(where, desc, *xs):
     """Device pointers of tensors, ints or None. A tensor that is not on the
-    current CUDA device is refused: the library launches on that device."""
+    current CUDA device is refused, and so is a block table that the descriptor
+    was made with: the library launches on that device."""
     global _current_device
     if _current_device is None:
         import torch
@@ -303,6 +304,11 @@ def _device_ptrs(where, *xs):
         current = _current_device()
     except (RuntimeError, AssertionError):        # no CUDA device, or no CUDA in torch
         current = -2
+    table = getattr(desc, "table_device", None)
+    if table is not None and table != current:
+        raise ValueError(f"{where}: the block table lies "
+                         f"{'in host memory' if table < 0 else f'on CUDA device {table}'}, the current "
+                         f"CUDA device is {current if current >= 0 else 'none'}")
     # get_device() is -1 for host memory
     return [x if x is None or x.__class__ is int else
             x.data_ptr() if x.get_device() == current else _other_device(where, x, current)
@@ -319,13 +325,24 @@ def make_paged_cache(page_size, pages_per_seq, num_pages, block_table, *, num_se
                      head_stride=None):
     """A paged cache. The strides default to pools [num_pages, page_size,
     H_kv, D]; block_table: int32 [num_seqs, pages_per_seq], kept alive by the
-    caller while descriptors made of this one are used."""
-    return dsa_paged_cache_t(num_seqs=num_seqs, H_kv=H_kv, D=D, page_size=page_size,
-                             pages_per_seq=pages_per_seq, num_pages=num_pages, dtype=dtype,
-                             page_stride=page_size * H_kv * D if page_stride is None else page_stride,
-                             slot_stride=H_kv * D if slot_stride is None else slot_stride,
-                             head_stride=D if head_stride is None else head_stride,
-                             block_table=_ptr(block_table))
+    caller while descriptors made of this one are used. Calls refuse a table
+    that is not on the current CUDA device, as they do other tensors."""
+    c = dsa_paged_cache_t(num_seqs=num_seqs, H_kv=H_kv, D=D, page_size=page_size,
+                          pages_per_seq=pages_per_seq, num_pages=num_pages, dtype=dtype,
+                          page_stride=page_size * H_kv * D if page_stride is None else page_stride,
+                          slot_stride=H_kv * D if slot_stride is None else slot_stride,
+                          head_stride=D if head_stride is None else head_stride,
+                          block_table=_ptr(block_table))
+    if hasattr(block_table, "get_device"):
+        c.table_device = block_table.get_device()
+    return c
+
+
+def _of_cache(desc, cache):
+    """`desc` with what the cache's descriptor says beside its C fields, which
+    are copied without it."""
+    desc.table_device = getattr(cache, "table_device", None)
+    return desc
 
 
 def make_append_desc(cache, T, H, rope_dim, *, rope_style=DSA_ROPE_INTERLEAVED,
@@ -333,43 +350,43 @@ def make_append_desc(cache, T, H, rope_dim, *, rope_style=DSA_ROPE_INTERLEAVED,
     """Strides: elements between consecutive tokens of q, k and v (default:
     contiguous [T, heads, D])."""
     kv = cache.H_kv * cache.D
-    return dsa_append_desc_t(cache=cache, T=T, H=H, rope_dim=rope_dim, rope=rope_style,
-                             q_dtype=q_dtype, q_stride=H * cache.D if q_stride is None else q_stride,
-                             k_stride=kv if k_stride is None else k_stride,
-                             v_stride=kv if v_stride is None else v_stride)
+    return _of_cache(dsa_append_desc_t(
+        cache=cache, T=T, H=H, rope_dim=rope_dim, rope=rope_style, q_dtype=q_dtype,
+        q_stride=H * cache.D if q_stride is None else q_stride,
+        k_stride=kv if k_stride is None else k_stride,
+        v_stride=kv if v_stride is None else v_stride), cache)
 
 
 def dsa_cache_append(desc, q, k, v, cos, sin, positions, seq_ids, q_out, q_scale, k_cache,
                      k_scale, v_cache, v_scale, stream=None) -> int:
     return _check(_lib.dsa_cache_append(
-        ctypes.byref(desc), *_device_ptrs("dsa_cache_append", q, k, v, cos, sin, positions, seq_ids,
-                                          q_out, q_scale, k_cache, k_scale, v_cache, v_scale),
+        ctypes.byref(desc), *_device_ptrs("dsa_cache_append", desc, q, k, v, cos, sin, positions,
+                                          seq_ids, q_out, q_scale, k_cache, k_scale, v_cache, v_scale),
         stream), "dsa_cache_append")
 
 
 def make_block_pool_desc(cache, block_size, S_pool, *, seq_stride=None, head_stride=None):
     """The strides default to pooled rows [num_seqs, H_kv, S_pool, D]."""
     head = S_pool * cache.D if head_stride is None else head_stride
-    return dsa_block_pool_desc_t(cache=cache, block_size=block_size, S_pool=S_pool,
-                                 seq_stride=cache.H_kv * head if seq_stride is None else seq_stride,
-                                 head_stride=head)
+    return _of_cache(dsa_block_pool_desc_t(
+        cache=cache, block_size=block_size, S_pool=S_pool,
+        seq_stride=cache.H_kv * head if seq_stride is None else seq_stride, head_stride=head), cache)
 
 
 def dsa_block_pool(desc, k_cache, k_scale, start, positions, pooled, pooled_scale, last_block=None,
                    stream=None) -> int:
     return _check(_lib.dsa_block_pool(
-        ctypes.byref(desc), *_device_ptrs("dsa_block_pool", k_cache, k_scale, start, positions,
-                                          pooled, pooled_scale, last_block), stream),
+        ctypes.byref(desc), *_device_ptrs("dsa_block_pool", desc, k_cache, k_scale, start,
+                                          positions, pooled, pooled_scale, last_block), stream),
         "dsa_block_pool")
 
 
 def make_paged_attention_desc(cache, T, H, sm_scale, *, window=0, block_size=0, num_blocks=0,
                               block_heads=1, flags=0, wait_limit_ns=0):
     """block_size and num_blocks: for dsa_block_attention_forward."""
-    return dsa_paged_attention_desc_t(cache=cache, T=T, H=H, sm_scale=sm_scale, window=window,
-                                      block_size=block_size, num_blocks=num_blocks,
-                                      block_heads=block_heads, flags=flags,
-                                      wait_limit_ns=wait_limit_ns)
+    return _of_cache(dsa_paged_attention_desc_t(
+        cache=cache, T=T, H=H, sm_scale=sm_scale, window=window, block_size=block_size,
+        num_blocks=num_blocks, block_heads=block_heads, flags=flags, wait_limit_ns=wait_limit_ns), cache)
 
 
 def dsa_paged_attention_workspace_size(desc) -> int:
@@ -382,14 +399,14 @@ def dsa_paged_attention_workspace_size(desc) -> int:
 def dsa_paged_attention_forward(desc, q, k, k_scale, v, v_scale, sinks, positions, seq_ids, out,
                                 lse, workspace, workspace_bytes, stream=None) -> int:
     return _check(_lib.dsa_paged_attention_forward(
-        ctypes.byref(desc), *_device_ptrs("dsa_paged_attention_forward", q, k, k_scale, v, v_scale,
-                                          sinks, positions, seq_ids, out, lse, workspace),
+        ctypes.byref(desc), *_device_ptrs("dsa_paged_attention_forward", desc, q, k, k_scale, v,
+                                          v_scale, sinks, positions, seq_ids, out, lse, workspace),
         workspace_bytes, stream), "dsa_paged_attention_forward")
 
 
 def dsa_block_attention_forward(desc, q, k, k_scale, v, v_scale, sinks, positions, seq_ids, blocks,
                                 out, lse, workspace, workspace_bytes, stream=None) -> int:
     return _check(_lib.dsa_block_attention_forward(
-        ctypes.byref(desc), *_device_ptrs("dsa_block_attention_forward", q, k, k_scale, v, v_scale,
-                                          sinks, positions, seq_ids, blocks, out, lse, workspace),
+        ctypes.byref(desc), *_device_ptrs("dsa_block_attention_forward", desc, q, k, k_scale, v,
+                                          v_scale, sinks, positions, seq_ids, blocks, out, lse, workspace),
         workspace_bytes, stream), "dsa_block_attention_forward")

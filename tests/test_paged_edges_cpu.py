@@ -95,3 +95,68 @@ def test_attention_flags():
     t = dsa.dsa_paged_attention_desc_t
     assert t.flags.offset == t.block_heads.offset + 4 and t.wait_limit_ns.offset == t.block_heads.offset + 8
     assert ctypes.sizeof(t) == t.wait_limit_ns.offset + 8
+
+
+def _calls(dsa, cache):
+    """Every call of the paged operators on fake pointers that fail no check."""
+    f = 1 << 20
+    attn = dsa.make_paged_attention_desc(cache, 3, 4, 0.1)
+    listed = dsa.make_paged_attention_desc(cache, 3, 4, 0.1, block_size=64, num_blocks=4)
+    return {
+        "dsa_cache_append": lambda: dsa.dsa_cache_append(
+            dsa.make_append_desc(cache, 3, 4, 0), f, f, f, None, None, f, None, 2 * f, None, f, None, f, None),
+        "dsa_block_pool": lambda: dsa.dsa_block_pool(
+            dsa.make_block_pool_desc(cache, 4, 8), f, None, None, f, f, None),
+        "dsa_paged_attention_forward": lambda: dsa.dsa_paged_attention_forward(
+            attn, f, f, None, f, None, None, f, None, f, None, f, 1 << 30),
+        "dsa_block_attention_forward": lambda: dsa.dsa_block_attention_forward(
+            listed, f, f, None, f, None, None, f, None, f, f, None, f, 1 << 30)}
+
+
+@pytest.mark.parametrize("current,where", [(0, "host"), (1, "cuda0"), (None, "host")])
+def test_a_block_table_of_another_device_is_refused(monkeypatch, current, where):
+    """The descriptors remember where their table lies: a call on another device
+    (or on none) is refused before anything else is looked at."""
+    import torch
+
+    import sparse_attention_lightning_tcgen05_b200 as dsa
+
+    class OnDevice0:                                # stands in for a CUDA tensor
+        def get_device(self):
+            return 0
+
+        def data_ptr(self):
+            return 1 << 20
+
+    def device():
+        if current is None:
+            raise RuntimeError("no CUDA device")
+        return current
+    monkeypatch.setattr(dsa, "_current_device", device)
+    table = torch.zeros((2, 16), dtype=torch.int32) if where == "host" else OnDevice0()
+    cache = dsa.make_paged_cache(64, 16, 40, table, num_seqs=2, H_kv=2)
+    for name, call in _calls(dsa, cache).items():
+        with pytest.raises(ValueError, match=name + ".*block table"):
+            call()
+
+
+def test_a_block_table_of_the_current_device_or_a_pointer_is_taken(monkeypatch):
+    import torch
+
+    import sparse_attention_lightning_tcgen05_b200 as dsa
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are fake")
+    monkeypatch.setattr(dsa, "_current_device", lambda: 0)
+
+    class OnDevice0:
+        def get_device(self):
+            return 0
+
+        def data_ptr(self):
+            return 1 << 20
+    for table in (OnDevice0(), 1 << 20):
+        cache = dsa.make_paged_cache(64, 16, 40, table, num_seqs=2, H_kv=2)
+        for call in _calls(dsa, cache).values():
+            with pytest.raises(dsa.DsaError) as e:  # past every check: no device
+                call()
+            assert e.value.status == dsa.DSA_ERR_CUDA
