@@ -10,6 +10,7 @@ raises if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -142,12 +143,12 @@ for _f in EXPORTS[:-1]:
 
 
 def _ptr(x) -> int | None:
-    """A device pointer from a torch tensor, an int, or None."""
+    """A device pointer from a torch tensor, an int (numpy's too), or None."""
     if x is None:
         return None
     if isinstance(x, int):
         return x
-    return x.data_ptr()
+    return x.data_ptr() if hasattr(x, "data_ptr") else operator.index(x)
 
 
 def make_desc(T, H, index_topk, *, D=128, S=0, k_seq_stride=0, num_seqs=0,
@@ -293,8 +294,8 @@ _current_device = None
 
 
 def _device_ptrs(where, desc, *xs):
-    """Device pointers of tensors, ints or None. A tensor that is not on the
-    current CUDA device is refused, and so is a block table that the descriptor
+    """Device pointers of tensors, ints (numpy's too) or None. A tensor that is not
+    on the current CUDA device is refused, and so is a block table that the descriptor
     was made with: the library launches on that device."""
     global _current_device
     if _current_device is None:
@@ -310,9 +311,13 @@ def _device_ptrs(where, desc, *xs):
                          f"{'in host memory' if table < 0 else f'on CUDA device {table}'}, the current "
                          f"CUDA device is {current if current >= 0 else 'none'}")
     # get_device() is -1 for host memory
-    return [x if x is None or x.__class__ is int else
-            x.data_ptr() if x.get_device() == current else _other_device(where, x, current)
-            for x in xs]
+    try:
+        return [x if x is None or x.__class__ is int else
+                x.data_ptr() if x.get_device() == current else _other_device(where, x, current)
+                for x in xs]
+    except AttributeError:                        # neither a tensor nor Python's int
+        return _device_ptrs(where, desc, *[x if x is None or hasattr(x, "get_device") else
+                                           operator.index(x) for x in xs])
 
 
 def _other_device(where, x, current):

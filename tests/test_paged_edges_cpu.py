@@ -160,3 +160,20 @@ def test_a_block_table_of_the_current_device_or_a_pointer_is_taken(monkeypatch):
             with pytest.raises(dsa.DsaError) as e:  # past every check: no device
                 call()
             assert e.value.status == dsa.DSA_ERR_CUDA
+
+
+def test_pointers_as_numpy_integers():
+    """They reach the library like Python's; what is no pointer is a TypeError."""
+    import numpy as np
+
+    import sparse_attention_lightning_tcgen05_b200 as dsa
+    f = np.int64(1 << 20)
+    cache = dsa.make_paged_cache(64, 16, 40, f, num_seqs=2, H_kv=2)
+    assert cache.block_table == 1 << 20
+    desc = dsa.make_block_pool_desc(cache, 4, 8)
+    with pytest.raises(dsa.DsaError) as e:          # pooled is misaligned, and seen to be
+        dsa.dsa_block_pool(desc, f, None, None, np.uint64(1 << 20), np.int64((1 << 20) + 8), None)
+    assert e.value.status == dsa.DSA_ERR_INVALID_ARG
+    for bad in (1.5, "pool"):
+        with pytest.raises(TypeError):
+            dsa.dsa_block_pool(desc, bad, None, None, f, f, None)
