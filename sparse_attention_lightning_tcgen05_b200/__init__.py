@@ -291,16 +291,18 @@ def dsa_indexer_prepare(desc, x, qr, wq_b, wk, weights_proj, k_norm_weight, k_no
 
 
 _current_device = None
+_TENSORS = ()
 
 
 def _device_ptrs(where, desc, *xs):
     """Device pointers of tensors, ints (numpy's too) or None. A tensor that is not
     on the current CUDA device is refused, and so is a block table that the descriptor
     was made with: the library launches on that device."""
-    global _current_device
+    global _current_device, _TENSORS
     if _current_device is None:
         import torch
         _current_device = torch.cuda.current_device
+        _TENSORS = (torch.Tensor,)
     try:
         current = _current_device()
     except (RuntimeError, AssertionError):        # no CUDA device, or no CUDA in torch
@@ -311,16 +313,18 @@ def _device_ptrs(where, desc, *xs):
                          f"{'in host memory' if table < 0 else f'on CUDA device {table}'}, the current "
                          f"CUDA device is {current if current >= 0 else 'none'}")
     # get_device() is -1 for host memory
-    try:
-        return [x if x is None or x.__class__ is int else
-                x.data_ptr() if x.get_device() == current else _other_device(where, x, current)
-                for x in xs]
-    except AttributeError:                        # neither a tensor nor Python's int
-        return _device_ptrs(where, desc, *[x if x is None or hasattr(x, "get_device") else
-                                           operator.index(x) for x in xs])
+    return [x if x is None or x.__class__ is int else
+            x.data_ptr() if x.__class__ in _TENSORS and x.get_device() == current else
+            _other_ptr(where, x, current) for x in xs]
 
 
-def _other_device(where, x, current):
+def _other_ptr(where, x, current):
+    """The pointer of what is neither None, an int nor a plain tensor on the
+    current device."""
+    if not hasattr(x, "get_device"):
+        return operator.index(x)
+    if x.get_device() == current:
+        return x.data_ptr()
     raise ValueError(f"{where}: a tensor on {x.device}, the current CUDA device is "
                      f"{current if current >= 0 else 'none'}")
 

@@ -177,3 +177,15 @@ def test_pointers_as_numpy_integers():
     for bad in (1.5, "pool"):
         with pytest.raises(TypeError):
             dsa.dsa_block_pool(desc, bad, None, None, f, f, None)
+
+
+def test_what_only_looks_like_a_tensor_ends_with_an_error(monkeypatch):
+    import sparse_attention_lightning_tcgen05_b200 as dsa
+
+    class NoPointer:
+        def get_device(self):
+            return 0
+    monkeypatch.setattr(dsa, "_current_device", lambda: 0)
+    cache = dsa.make_paged_cache(64, 16, 40, 1 << 20, num_seqs=2, H_kv=2)
+    with pytest.raises(AttributeError):
+        dsa.dsa_block_pool(dsa.make_block_pool_desc(cache, 4, 8), NoPointer(), None, None, 1 << 20, 1 << 20, None)
