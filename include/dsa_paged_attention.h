@@ -25,8 +25,10 @@
  * and infinities among it, has no effect; a NaN that is kept gives NaN, and beside
  * other slots so may an infinite value whose weight is 0. A weight
  * e^{l_s} takes part as a bf16 number relative to its row's largest (one below
- * 2^-126 of that may count as 0); sums are fp32, of weights up to 2^8 times the
- * final largest one: values of 2^100 and more may make them overflow.
+ * 2^-126 of that may count as 0), and over an fp8 cache under up to 48 heads so
+ * does its product with the value's scale, so that scales below 2^-107 lose bits
+ * of small weights; sums are fp32, of weights up to 2^8 times the final largest
+ * one: values of 2^100 and more may make them overflow.
  *
  * Where the operation is defined (page titles and sections):
  *  - NeMo AutoModel optimized_kernels, sparse_attention_torch and

@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
           }
         }
       } else {
-        // the slots' scales go into P: one set of fragments per 32 features
+        // the slots' scales go into P: one set of fragments per 32 features (exact
+        // where the product is 2^-126 or more: bf16 keeps its bits from there on)
         const uint32_t *const sc =
             reinterpret_cast<const uint32_t *>(smem + Smem::off_scale + st * Smem::kScaleBytes) + kStep;
 #pragma unroll

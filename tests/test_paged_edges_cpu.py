@@ -189,3 +189,34 @@ def test_what_only_looks_like_a_tensor_ends_with_an_error(monkeypatch):
     cache = dsa.make_paged_cache(64, 16, 40, 1 << 20, num_seqs=2, H_kv=2)
     with pytest.raises(AttributeError):
         dsa.dsa_block_pool(dsa.make_block_pool_desc(cache, 4, 8), NoPointer(), None, None, 1 << 20, 1 << 20, None)
+
+
+def test_every_scale_byte_decides_outputs():
+    """The check of attention over the chosen scales sees each of them: with the
+    values of any one byte of a sequence left out of the oracle, or off by a step of
+    the scale, the exact outputs fail it."""
+    import numpy as np
+    import torch
+
+    import oracle.paged as orc
+    from paged_scales import BY_BLOCK, BY_SLOT, POSITIONS, scaled_cache
+    from paged_util import bf16_bits, check_attention
+    rng = np.random.default_rng(66)
+    c, byte = scaled_cache(rng)
+    q = rng.standard_normal((c.num_seqs, 2, 128))
+    k, v = c.rows("k"), c.rows("v")
+    assert np.isfinite(v).all()
+
+    def attention(values, i):
+        return orc.attention(q[i:i + 1], k, values, c.table[i:i + 1], POSITIONS[i:i + 1], None, 128 ** -0.5)
+    tried = 0
+    for i, bytes_ in enumerate(BY_BLOCK + BY_SLOT):
+        exact = attention(v, i)
+        out, lse = bf16_bits(exact[0]), torch.from_numpy(exact[1]).float()
+        check_attention(out, lse, exact)
+        for b in set(bytes_):
+            for wrong in (0.0, 0.5, 2.0):
+                with pytest.raises(AssertionError):
+                    check_attention(out, lse, attention(np.where(byte == b, wrong * v, v), i))
+                tried += 1
+    assert tried > 100

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import oracle.paged as orc
+from paged_scales import POSITIONS, scaled_cache
 from paged_util import D, Cache, attend, bf16_bits, check_attention, decode_mx, dev_i32
 
 pytestmark = pytest.mark.gpu
@@ -225,3 +226,36 @@ def test_a_stalled_call_reports_the_timeout(dsa, H, fp8, T, listed):
         got = attend(dsa, c, dev, table, qc, pos, SCALE, seq_ids=seq, workspace=ws, **kw)
     ref = orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, seq, SCALE, **kw)
     check_attention(*got, ref)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("G", [8, 40, 64, 128])
+def test_fp8_value_scales_one_by_one(dsa, G, listed):
+    """Scale bytes from 20 to 218, each deciding outputs of its own (a CPU test
+    shows that the check sees every one): one byte a feature block, blocks that differ
+    by up to 2^198, and slots around the border of the two-step conversion."""
+    rng = np.random.default_rng(66)
+    c, _ = scaled_cache(rng)
+    dev, table = c.to("cuda")
+    q = queries(rng, c.num_seqs, G)
+    kw = {}
+    if listed:
+        kw = dict(blocks=np.tile(np.array([2, 0, 5, -1, 1, 7]), (c.num_seqs, 1, 1)), block_size=16, window=16)
+    out, lse = attend(dsa, c, dev, table, q.cuda(), POSITIONS, SCALE, **kw)
+    check_attention(out, lse, orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, POSITIONS, None,
+                                            SCALE, **kw))
+
+
+@pytest.mark.parametrize("G", [8, 64])
+@pytest.mark.parametrize("byte", [20, 60, 110, 132, 133, 134, 135, 160, 200])
+def test_fp8_key_scales(dsa, G, byte):
+    """Keys under two neighbouring scale bytes, the logit scale the other way round,
+    so that the logits are ordinary ones."""
+    rng = np.random.default_rng(67 + byte)
+    c = Cache(rng, 4, 3, 64, 1, True)
+    scale = c.pools["k"][1]
+    scale[:] = torch.from_numpy(rng.integers(byte, byte + 2, len(scale)).astype(np.uint8))
+    dev, table = c.to("cuda")
+    q, pos, amp = queries(rng, 4, G), np.array([191, 60, 100, 127]), SCALE * 2.0 ** (121 - byte)
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, amp)
+    check_attention(out, lse, orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, None, amp))
