@@ -409,13 +409,15 @@ __device__ __forceinline__ PoolRaw<kFp8> pool_load(const PoolParams &p, int64_t 
   return r;
 }
 
-// acc += the row's features (fp8: under the scale byte number blk of e, as an fp32
-// exponent: 0 makes 0, and 255 an infinity, which makes NaN of the zeros beside
-// it)
+// acc += the row's features times `part`, a power of two that is at most the
+// share of a row in its block, so that a sum passes fp32's range only where the mean
+// does (fp8: under the scale byte number blk of e, as an fp32 exponent: 0 makes 0,
+// and 255 an infinity, which makes NaN of the zeros beside it)
 template <bool kFp8>
-__device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &r, uint32_t e, int blk) {
+__device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &r, uint32_t e, int blk,
+                                         float part) {
   if constexpr (kFp8) {
-    const float f = __uint_as_float(__byte_perm(e, 0, blk << 12 | 0x444) >> 1);
+    const float f = __uint_as_float(__byte_perm(e, 0, blk << 12 | 0x444) >> 1) * part;
     const uint32_t q[4] = {r.w.x & 0xffffu, r.w.x >> 16, r.w.y & 0xffffu, r.w.y >> 16};
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = ffma2(e4m3x2_f32(q[i]), make_float2(f, f), acc[i]);
@@ -423,10 +425,8 @@ __device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &
     float v[8];
     unpack8(r.w, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[i].x += v[2 * i];
-      acc[i].y += v[2 * i + 1];
-    }
+    for (int i = 0; i < 4; ++i)
+      acc[i] = ffma2(make_float2(v[2 * i], v[2 * i + 1]), make_float2(part, part), acc[i]);
   }
 }
 
@@ -456,7 +456,13 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
   const int per_cta = kPoolGroups / p.share;
   const int mine = grp / p.share, part_of = grp - mine * p.share;
   const bool warp_joins = (grp & ~1 & (p.share - 1)) == 0;  // a first half warp is in this warp
-  const float size = static_cast<float>(p.block_size), inv = 1.f / size;
+  // a power of two's reciprocal is the mean's whole factor; else the power of two
+  // below it, and the sum over the rest of the size (above 1/2) is the same quotient
+  const float size = static_cast<float>(p.block_size);
+  const float part_of_sum = kR > 0 && kR < kPoolRun ? 1.f / (kR > 0 ? kR : 1)
+                            : kR > 0                ? 1.f / size
+                                                    : 1.f / static_cast<float>(2 << (31 - __clz(p.block_size)));
+  const float rest = size * part_of_sum;
   int turn = 0;
   for (int seq0 = 0; seq0 < p.g.num_seqs; seq0 += kPoolSeqs) {
     const int seqs = min(kPoolSeqs, p.g.num_seqs - seq0);
@@ -565,15 +571,15 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
           for (int u = 0; u < kPoolRun; ++u) {
             uint32_t e = 0;
             if constexpr (kFp8) e = __shfl_sync(0xffffffffu, sc, u, kPoolLanes);
-            pool_add<kFp8>(acc, w[u], e, l >> 2);
+            pool_add<kFp8>(acc, w[u], e, l >> 2, part_of_sum);
             if (kR < 16 && u % (kR > 0 ? kR : 1) == kR - 1) {
-              // a block ends; its size is a power of two: the product is the quotient
+              // a block ends
               const int b = cur.b0 + u / (kR > 0 ? kR : 1);
               float x[8];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                x[2 * i] = acc[i].x * (1.f / (kR > 0 ? kR : 1));
-                x[2 * i + 1] = acc[i].y * (1.f / (kR > 0 ? kR : 1));
+                x[2 * i] = acc[i].x;
+                x[2 * i + 1] = acc[i].y;
                 acc[i] = make_float2(0.f, 0.f);
               }
               pool_store<kFp8>(x, p, cur.seq, cur.h, b, l, in && b >= cur.lo && b < cur.hi);
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
             }
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) pool_add<kFp8>(acc, w[u], e[u], 0);
+          for (int u = 0; u < 4; ++u) pool_add<kFp8>(acc, w[u], e[u], 0, part_of_sum);
         }
         next = locate(it0 + per_cta + mine);
       }
@@ -625,9 +631,8 @@ __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // a power of two's reciprocal gives the same quotient
-          x[2 * i] = kR > 0 ? acc[i].x * inv : __fdiv_rn(acc[i].x, size);
-          x[2 * i + 1] = kR > 0 ? acc[i].y * inv : __fdiv_rn(acc[i].y, size);
+          x[2 * i] = kR > 0 ? acc[i].x : __fdiv_rn(acc[i].x, rest);
+          x[2 * i + 1] = kR > 0 ? acc[i].y : __fdiv_rn(acc[i].y, rest);
         }
         pool_store<kFp8>(x, p, cur.seq, cur.h, cur.b0, l, cur.hi > cur.lo && part_of == 0);
       }

@@ -259,3 +259,32 @@ def test_fp8_key_scales(dsa, G, byte):
     q, pos, amp = queries(rng, 4, G), np.array([191, 60, 100, 127]), SCALE * 2.0 ** (121 - byte)
     out, lse = attend(dsa, c, dev, table, q.cuda(), pos, amp)
     check_attention(out, lse, orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, None, amp))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("bs", [1, 2, 3, 4, 7, 16, 32, 63, 64])
+def test_pooling_keys_near_the_largest_number(dsa, bs, fp8):
+    """The mean of keys of up to bf16's largest number is as finite as they are:
+    within the fp32 sum's rounding (bs + 1 half steps of the largest) and its own
+    (2^-8, or 2^-4 for e4m3)."""
+    rng = np.random.default_rng(68)
+    c = Cache(rng, 2, 2, 64, 1, fp8, values=False)
+    if fp8:
+        data, scale = c.pools["k"]
+        data[:] = torch.from_numpy(rng.integers(0x70, 0x7f, len(data)).astype(np.uint8))    # 128 .. 448
+        scale[:] = 246                                                                        # 2^119
+    else:
+        top = float(torch.finfo(torch.bfloat16).max)
+        c.set_rows("k", rng.uniform(0.3, 1.0, (c.num_pages, 64, 1, D)) * top)
+    dev, table = c.to("cuda")
+    n, pos = 128 // bs, [127, 100]
+    pooled = torch.zeros((2, n, D), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    pscale = torch.zeros((2, n, D // 32), dtype=torch.uint8, device="cuda") if fp8 else None
+    dsa.dsa_block_pool(dsa.make_block_pool_desc(c.desc(dsa, table), bs, n), *dev["k"], None, dev_i32(pos), pooled,
+                       pscale, None, torch.cuda.current_stream().cuda_stream)
+    got = decode_mx(pooled.cpu(), pscale.cpu()) if fp8 else pooled.double().cpu().numpy()
+    rows, _ = orc.pool_blocks(c.rows("k"), c.table, None, pos, bs, n)
+    assert len(rows) == 128 // bs + 101 // bs
+    for (i, b), ref in rows.items():
+        slack = (bs + 1) * 2.0 ** -24 * np.abs(ref).max()
+        assert np.all(np.abs(got[i, b] - ref[0]) <= (2.0 ** -4 if fp8 else 2.0 ** -8) * np.abs(ref[0]) + 2 * slack)
