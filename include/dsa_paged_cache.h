@@ -30,7 +30,8 @@
  * block_size - 1, the last complete block (-1: none). The pooled rows are a
  * key cache that dsa_indexer_forward scores: with one row per (sequence,
  * head), positions = last_block (DSA_MASK_POSITIONS, k_seq_stride =
- * head_stride where the rows are evenly spaced); for one sequence's prefill,
+ * head_stride where the rows are evenly spaced, for an fp8 cache a multiple of
+ * 512 as the indexer has it); for one sequence's prefill,
  * DSA_MASK_COMPRESSED with compress_ratio = block_size. Its index sets are
  * block lists of dsa_block_attention_forward (dsa_paged_attention.h).
  *

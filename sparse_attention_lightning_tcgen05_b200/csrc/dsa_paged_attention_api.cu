@@ -52,15 +52,18 @@ dsa_status_t check_attn(const dsa_paged_attention_desc_t *d, bool list) {
 // one tcgen05 tile, from more than 16 of them on (the other kernel takes 16 at a
 // time, each time with all the slots), for an fp8 cache from more than 48 on:
 // there the conversion bounds the wide kernel whatever the heads. Contexts with
-// one key head, us, other kernel / wide:
+// one key head, us (graph replays, three inputs in turn), other kernel / wide:
 //   heads               16         32         48         64        128
-//   bf16 4 x 65,536  32 / 35    36 / 35    68 / 36    59 / 37   109 / 39
-//        16 x 4,096  14 / 23    19 / 23    21 / 25    24 / 26    32 / 31
-//   fp8  4 x 65,536  24 / 53    35 / 53    49 / 54    60 / 54   110 / 55
-//        16 x 4,096  18 / 31    22 / 32    24 / 33    27 / 35    39 / 39
-// Lengths are not known on the host; what the wide kernel loses on short
-// contexts is a few us, what it gains on many long ones is the larger part (64
-// contexts of 1,024 to 32,768 slots, 2 key heads of 32 heads, bf16: 315 / 194).
+//   bf16 4 x 65,536  32 / 35    37 / 35    68 / 36    60 / 37   109 / 39
+//        16 x 4,096  16 / 24    21 / 25    23 / 27    26 / 29    35 / 34
+//        16 x 1,024  10 / 13    15 / 13    15 / 13    16 / 14    18 / 14
+//   fp8  4 x 65,536  25 / 53    35 / 54    49 / 55    61 / 55   111 / 55
+//        16 x 4,096  15 / 30    21 / 32    24 / 33    26 / 34    38 / 40
+//        16 x 1,024  14 / 16    16 / 16    16 / 17    17 / 17    21 / 18
+// Of the lengths the host knows the table's capacity alone; what the wide kernel
+// loses between short and long ones is a few us, what it gains on many long ones is
+// the larger part (64 contexts of 1,024 to 32,768 slots, 2 key heads of 32 heads,
+// bf16: 315 / 195).
 struct Plan {
   bool fp8, wide;
   int rows, head_tiles, step, grid;      // grid: CTAs at most
@@ -193,9 +196,11 @@ dsa_status_t attend(const dsa_paged_attention_desc_t *d, bool list, const void *
   int grid = static_cast<int>(std::min(most, want));
   // A multiple of the key heads, where that idles less than a sixteenth of the
   // CTAs: the heads' shares then begin alike, and what lies side by side in
-  // memory (a slot's rows and scales of all heads) is read at the same time. 64
-  // contexts of 1,024 to 32,768 slots, 4 key heads, fp8: 251 us otherwise, 243 so;
-  // 16 contexts, 8 key heads, bf16: 179 and 173.
+  // memory (a slot's rows and scales of all heads) is read at the same time. (2, 4
+  // and 8 key heads divide the 296 CTAs anyhow.) 16 contexts of 2,048 to 32,768 slots,
+  // 8 query heads a key head, us otherwise and so: bf16 with 3, 6, 7, 12, 16 key
+  // heads 84 and 84, 144 and 144, 165 and 163, 267 and 263, 355 and 340; fp8 63 and
+  // 63, 102 and 101, 118 and 114, 180 and 182, 230 and 237.
   if (grid % p.g.H_kv * 16 < grid) grid -= grid % p.g.H_kv;
   p.chain_by_item = items <= grid;
   p.ctas = grid;

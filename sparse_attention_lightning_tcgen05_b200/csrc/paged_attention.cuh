@@ -113,8 +113,8 @@ struct PaItem {
 template <bool kFp8>
 struct PaSmem {
   static constexpr int kStep = kFp8 ? 32 : 16;
-  // Consumer warps: 12 warps an SM have the same 168 registers as 10. fp8, the
-  // batch above: five with two stages each 241 us, four with three 250; bf16: 189
+  // Consumer warps: 12 warps an SM have the same 168 registers as 10. The fp8
+  // batch below: five with two stages each 241 us, four with three 250; bf16: 189
   // and 175, where the fewer stages cost more than the fifth warp brings.
   static constexpr int kWarps = kFp8 ? 5 : 4;
   static constexpr int kThreads = (kWarps + 1) * 32;                // and the producer
@@ -157,13 +157,14 @@ struct PaSmem {
 // also leave each warp its softmax in registers, where tcgen05 would spend its
 // 128 rows on 16 heads and take a trip through TMEM a tile. Two CTAs an SM with
 // 192 KB (bf16) of stages between them cover HBM's latency. Measured on a B200:
-// 16 contexts of 2,048 to 32,768 slots, 8 key heads, bf16: 171 to 175 us, 6.7 TB/s
-// (HBM); 64 contexts of 1,024 to 32,768, 4 key heads, fp8: 228 to 250 us, 4.9 to 4.6
-// TB/s, bound by the chain from a stage's bytes to fragments (about 700 instructions
-// a step of 32 slots; the loads alone take 181 us). One context of 1,000 slots: 11.3
-// us, a chain of launches, prologue, loads, hand-over and join. 1,024 tokens that
-// each list 16 blocks of 64 and the last 64 slots: 234 us, of them 9.1 a block (2 GB
-// through the L2 in all, 13.9 TB/s), 15 fixed and 25 for the items' ends.
+// (calls one by one; graph replays in brackets) 16 contexts of 2,048 to 32,768
+// slots, 8 key heads, bf16: 176 us (173), 6.6 TB/s, HBM; 64 contexts of 1,024 to
+// 32,768, 4 key heads, fp8: 249 us (216), 4.6 TB/s, bound by the chain from a stage's
+// bytes to fragments (about 700 instructions a step of 32 slots; the loads alone take
+// 181 us). One context of 1,000 slots: 12.2 us (11.6), a chain of launches, prologue,
+// loads, hand-over and join. 1,024 tokens that each list 16 blocks of 64 and the last
+// 64 slots: 233 us (208), of them 9.1 a block (2 GB through the L2 in all, 13.9 TB/s),
+// 15 fixed and 25 for the items' ends.
 template <bool kFp8, bool kList>
 __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -736,10 +737,10 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
 // a 4-feature piece a lane, each over every kWays-th partial with kBatch of
 // them in flight, added up through shared memory in warp order. Eight ways
 // where items are few and their partials many (4 contexts of 65,000 to 131,072
-// slots under 128 heads, 37 partials an item: the whole call 70 us by one warp a
-// head, 57 so); one way, and fewer blocks, where most items lie in one or two
-// CTAs (16 contexts of 2,048 to 32,768 slots, 8 key heads: 185 us by eight ways,
-// 178 by one).
+// slots under 128 heads, 37 partials an item: the whole call 66 us by one warp a
+// head, 61 so); one way, and fewer blocks, where most items lie in one or two
+// CTAs (16 contexts of 2,048 to 32,768 slots, 8 key heads: 183 us by eight ways,
+// 176 by one; 64 contexts, fp8: 260 and 249).
 constexpr int kPaJoinThreads = 512;
 template <int kWays>
 constexpr int kPaJoinHeads = kPaJoinThreads / 32 / kWays;     // of a block

@@ -19,10 +19,10 @@
 // (e4m3 times a power of two is exact in bf16); the rest is as for bf16.
 //
 // Measured on a B200 with 128 heads: 4 contexts of 65,000 to 131,072 slots, bf16:
-// 56 us, of them 18 fixed (launches, prologue, hand-over, join) and the rest HBM's
-// rate; 4 x 65,536 slots, fp8: 55 us (63 with two converting warps; 40 without
-// the conversion, 40 without the softmax, 34 without both: they share the issue
-// slots, and a staged tile waits for both).
+// 61 us, in graph replays 57, of them 18 fixed (launches, prologue, hand-over, join)
+// and the rest HBM's rate; 4 x 65,536 slots in graph replays: bf16 39 us, fp8 55 (63
+// with two converting warps; 40 without the conversion, 40 without the softmax, 34
+// without both: they share the issue slots, and a staged tile waits for both).
 #pragma once
 
 #include <cstdint>

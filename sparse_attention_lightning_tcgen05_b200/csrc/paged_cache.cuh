@@ -176,9 +176,9 @@ constexpr int kAppendLanes = kFp8 ? 8 : 16;
 // sines it reads once; four rows' loads are in flight a lane. Products and sums
 // of the rotation are rounded one by one (no fma), so that the result is the
 // formula's in fp32. Measured on a B200: 16 tokens (64 query heads, 8 key heads)
-// 2.4 us, a launch; 8,192 tokens bf16 65 us, 5.2 TB/s (copying reaches 6.6);
-// 12,345 tokens' 64 query heads and one key head to fp8 71 us, 4.4 TB/s, bound by
-// instructions (one group of 16 features a lane costs about 60).
+// 2.5 us in a graph, a launch; 8,192 tokens bf16 65 us, 5.2 TB/s (copying reaches
+// 6.6); 12,345 tokens' 64 query heads and one key head to fp8 74 us, 4.2 TB/s, bound
+// by instructions (with an fma for a product and the sum 72 us, bf16 64).
 template <bool kQFp8, bool kKvFp8, bool kHalves>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendParams p) {
   constexpr int kLanes = kAppendLanes<kQFp8 || kKvFp8>;
@@ -439,10 +439,10 @@ __device__ __forceinline__ void pool_add(float2 (&acc)[4], const PoolRaw<kFp8> &
 // on, which `share` half warps sum and the first of them joins (in order, so
 // that the result does not depend on timing). kR = 0: any block size, each row
 // looked up by itself, four in flight. Measured on a B200: a step of 64 sequences
-// 5.5 us (the chain start, positions, table, row); 240,000 bf16 keys by fours 12.2
-// us on resident rows and 17 on rows not in L2, 4.7 TB/s; 1.1 million fp8 rows by 64s
-// 37 us, 3.8 TB/s, bound by instructions
-// (four conversions to f16x2, eight to fp32 and four packed fmas a lane and row).
+// 5.8 us (the chain start, positions, table, row), 3.9 in a graph; 240,000 bf16 keys
+// by fours 12.2 us on resident rows and 17 on rows not in L2, 4.7 TB/s; 1.1 million
+// fp8 rows by 64s 38 us, 3.8 TB/s, bound by instructions (four conversions to f16x2,
+// eight to fp32, four packed fmas and a scale's product a lane and row).
 template <bool kFp8, int kR>
 __global__ void __launch_bounds__(kPoolThreads, kPoolCtasPerSm<kFp8>)
     block_pool_kernel(const PoolParams p) {

@@ -46,8 +46,10 @@ struct PagedAttnParams {
   uint64_t wait_limit_ns, drain_limit_ns;
 };
 
-// The items' order is (key-value head, token, tile of query heads): tokens of one
-// sequence read the same slots, and one head's stay in L2 while they pass.
+// The items' order is (key-value head, token, tile of query heads): neighbouring
+// CTAs are at tokens of one sequence and one head, which read the same slots. All
+// heads pass at the same time, each in its share of the CTAs, so that L2 holds what
+// their tokens read of all of them.
 
 // A CTA's range of all items' steps, [begin, end) of `total`, one of `ctas` that
 // have any; and the key-value head it starts in.
