@@ -114,16 +114,22 @@ def peaks():
         return dict(hbm=6650.0, bf16=1590.0, bf16_sust=1400.0, src="fallback")
 
 
-# The device code of the kernels that bench.py times: what their profiles depend on.
-KERNEL_SOURCES = ("prepare_gemm.cuh", "row_rule.cuh", "score_kernel.cuh", "sm100_ptx.cuh",
-                  "sparse_mqa.cuh", "topk_causal.cuh", "topk_cluster.cuh", "topk_kernel.cuh",
-                  "topk_rows.cuh")
+# What profiles depend on: the device code of the kernels that bench.py times, and
+# the host code that chooses their grids, splits and tensor maps.
+KERNEL_SOURCES = ("cu_check.cuh", "dsa_indexer_api.cu", "dsa_launch.h", "dsa_prepare_api.cu",
+                  "dsa_sparse_mqa_api.cu", "prepare_gemm.cuh", "row_rule.cuh", "score_kernel.cuh",
+                  "sm100_ptx.cuh", "sparse_mqa.cuh", "topk_causal.cuh", "topk_cluster.cuh",
+                  "topk_kernel.cuh", "topk_rows.cuh")
+# The same of the paged cache's operators.
+PAGED_SOURCES = ("dsa_launch.h", "dsa_paged_attention_api.cu", "dsa_paged_cache_api.cu",
+                 "paged_attention.cuh", "paged_attention_wide.cuh", "paged_cache.cuh", "paged_geom.h",
+                 "paged_rows.h", "paged_schedule.cuh", "sm100_ptx.cuh")
 
 
-def source_hash() -> str:
+def source_hash(files=None) -> str:
     h = hashlib.sha256()
     cs = os.path.join(ROOT, "sparse_attention_lightning_tcgen05_b200", "csrc")
-    for f in KERNEL_SOURCES:
+    for f in files or KERNEL_SOURCES:
         h.update(open(os.path.join(cs, f), "rb").read())
     return h.hexdigest()[:16]
 
