@@ -6,6 +6,7 @@
  * For query token t at position p = positions[t] of sequence i = seq_ids[t],
  * head h and its key-value head g = h / (H / H_kv):
  *     l_s = sm_scale * q[t, h, :] . k(i, s, g)          for every kept slot s
+ *                      (the product of q and k in fp32, within its range)
  *     lse[t, h]    = ln sum_s e^{l_s}
  *     out[t, h, :] = sum_s e^{l_s} v(i, s, g) / (sum_s e^{l_s} + e^{sinks[h]})
  * The kept slots:

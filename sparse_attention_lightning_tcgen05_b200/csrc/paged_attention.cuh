@@ -13,7 +13,6 @@
 // step (2^-9 on average) of each weight, which averages out over the slots.
 #pragma once
 
-#include <cfloat>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -377,11 +376,11 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
     // ---- the query heads as matrix fragments ----
     uint32_t qf[8][4];
     // logit scale of rows r0, r0 + 8: a negative one's sign goes to the query, so
-    // that the largest product is the largest logit; 0 counts as the least normal
-    // number, so that a masked logit stays -infinity
+    // that the largest product is the largest logit; 0 counts as the least number
+    // above it, so that a masked logit stays -infinity
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const float scale = fabsf(p.scale_log2);
-    float xs[2] = {fmaxf(scale, FLT_MIN), fmaxf(scale, FLT_MIN)};
+    const float scale = fabsf(p.scale_log2), least = __int_as_float(1);
+    float xs[2] = {fmaxf(scale, least), fmaxf(scale, least)};
     {
       const uint8_t *const sq = smem + Smem::off_q;
       if constexpr (!kFp8) {
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(PaSmem<kFp8>::kThreads, 2)
           // inf and NaN stay as they are; 2^shift must be a normal number
           const int shift = top >= 0x7f80u || top == 0 ? 0 : max(-126, min(126, 13 - e));
           const float up = __int_as_float((shift + 127) << 23);
-          xs[i] = fmaxf(scale * __int_as_float((127 - shift) << 23), FLT_MIN);
+          xs[i] = fmaxf(scale * __int_as_float((127 - shift) << 23), least);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
 #pragma unroll

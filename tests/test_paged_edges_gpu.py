@@ -288,3 +288,22 @@ def test_pooling_keys_near_the_largest_number(dsa, bs, fp8):
     for (i, b), ref in rows.items():
         slack = (bs + 1) * 2.0 ** -24 * np.abs(ref).max()
         assert np.all(np.abs(got[i, b] - ref[0]) <= (2.0 ** -4 if fp8 else 2.0 ** -8) * np.abs(ref[0]) + 2 * slack)
+
+
+@pytest.mark.parametrize("amp", [2.0 ** -127, -2.0 ** -127, 2.0 ** -126])
+@pytest.mark.parametrize("G,fp8", [(8, False), (8, True), (64, False), (64, True)])
+def test_logit_scales_below_the_normal_numbers(dsa, G, fp8, amp):
+    """Products of query and key near fp32's largest number under a logit scale
+    near its smallest: ordinary logits."""
+    rng = np.random.default_rng(69)
+    c = Cache(rng, 3, 2, 64, 1, fp8)
+    if fp8:
+        c.pools["k"][1] += 58
+    else:
+        c.set_rows("k", c.rows("k") * 2.0 ** 60)
+    dev, table = c.to("cuda")
+    q, pos = queries(rng, 3, G, 2.0 ** 60), np.array([127, 70, 20])
+    largest = np.abs(c.rows("k")).reshape(-1, D) @ np.abs(q.double().numpy()).reshape(-1, D).T
+    assert largest.max() < torch.finfo(torch.float32).max      # no partial sum overflows
+    out, lse = attend(dsa, c, dev, table, q.cuda(), pos, amp)
+    check_attention(out, lse, orc.attention(q.double().numpy(), c.rows("k"), c.rows("v"), c.table, pos, None, amp))
